@@ -396,6 +396,94 @@ int nvfp4_moe_decode_host(const void* x, int32_t x_dtype, int32_t T, int32_t H, 
                           const int32_t* topk_ids, const float* topk_weights, int32_t topk, float* out,
                           int32_t n_threads, int32_t isa, int64_t* dropped);
 
+/* ---- Products with 8- and 16-bit weights over the same routing --------------------------
+ * For the parts of such a layer whose weights are not 4-bit: dense projections in int8 with
+ * a scale per token and per channel (the activations as nvfp4_quant_rows_i8 writes them),
+ * and experts in int8, bf16 or fp16 over the row order of nvfp4_moe_route, with the
+ * gradients of the latter.
+ *
+ * Row order: the rows of expert e are expert_offsets[e] <= r < expert_offsets[e+1], and
+ * sorted_pairs[r] = t * topk + j names their pair. Offsets must ascend within [0, rows]
+ * and start at 0 (as nvfp4_moe_route writes them); values outside are clamped, so no access
+ * leaves the arrays. With sorted_pairs, row r of the product reads row
+ * src(r) = sorted_pairs[r] / topk of x (x_rows tokens, rows == x_rows * topk), so x needs
+ * no permuted copy; a pair outside [0, rows) reads row 0. Without it (NULL; topk unused)
+ * x has `rows` rows in the sorted order and src(r) = r. Rows at and behind
+ * expert_offsets[E] (the dropped pairs) take no part, and their output rows are left as
+ * they were. sorted_pairs may hold anything there.
+ *
+ * w [E][N][K] row-major. out_dtype is any nvfp4_dtype: sums are fp32 (int32 for int8
+ * operands, exact) and are rounded once. Results are deterministic (fixed summation order
+ * for given sizes). No workspace. */
+
+/* Dense int8 linear: out[t][n] = (fp32(sum_k x[t][k] * w[n][k]) * x_scale[t]) * w_scale[n],
+ * the sum exact in int32. x int8 [T][K], x_scale float [T], w int8 [N][K], w_scale float
+ * [N]; any int8 values (-128 too). A NaN or infinite scale gives NaN or infinite outputs
+ * where the fp32 products do. T == 0 is a no-op.
+ * Errors: EINVAL for null or misaligned pointers (x, w, out 16-byte aligned), T < 0, N < 1,
+ * K < 1, unknown out_dtype; EUNSUPPORTED for K not a multiple of 16 or above 131056 (the
+ * int32 sum), N above 2^20, T above 2^30. */
+int nvfp4_linear_i8(const int8_t* x, const float* x_scale, int32_t T, const int8_t* w, const float* w_scale,
+                    int32_t N, int32_t K, void* out, int32_t out_dtype, void* stream);
+
+/* The same by expert: out[r][n] = (fp32(sum_k x[s][k] * w[e][n][k]) * x_scale[s]) *
+ * w_scale[e][n], s = src(r), e the expert of row r. x int8 [x_rows][K], x_scale float
+ * [x_rows], w int8 [E][N][K], w_scale float [E][N], out [rows][N].
+ * Errors: those of nvfp4_linear_i8, EINVAL for a null expert_offsets, E < 1, rows < 0 or
+ * rows, x_rows and topk that disagree, EUNSUPPORTED for E above 8192 or rows above 2^30. */
+int nvfp4_grouped_linear_i8(const int8_t* x, const float* x_scale, int32_t x_rows, const int8_t* w,
+                            const float* w_scale, const int32_t* expert_offsets, int32_t E,
+                            const int32_t* sorted_pairs, int32_t topk, int32_t rows, int32_t N, int32_t K, void* out,
+                            int32_t out_dtype, void* stream);
+
+/* Grouped linear with bf16 or fp16 operands (dtype, the same for x and w):
+ * out[r][n] = sum_k x[src(r)][k] * w[e][n][k]; x [x_rows][K], w [E][N][K], out [rows][N].
+ * rows == 0 is a no-op and may pass null tensors.
+ * Errors: EINVAL for null or misaligned pointers (x, w, out 16-byte aligned), sizes out of
+ * range or that disagree, unknown dtypes; EUNSUPPORTED for dtype F32, N or K not a multiple
+ * of 8 or above 2^20, E above 8192, rows above 2^30. */
+int nvfp4_grouped_linear(const void* x, int32_t x_rows, const void* w, int32_t dtype, const int32_t* expert_offsets,
+                         int32_t E, const int32_t* sorted_pairs, int32_t topk, int32_t rows, int32_t N, int32_t K,
+                         void* out, int32_t out_dtype, void* stream);
+
+/* Its gradient for the rows: dx[r][k] = sum_n dy[r][n] * w[e][n][k]; dy [rows][N] and w in
+ * dtype, dx [rows][K] in the sorted order. With a gathered x, the token's gradient is the
+ * sum of its slots: nvfp4_moe_combine without weights. Errors as nvfp4_grouped_linear. */
+int nvfp4_grouped_linear_dx(const void* dy, const void* w, int32_t dtype, const int32_t* expert_offsets, int32_t E,
+                            int32_t rows, int32_t N, int32_t K, void* dx, int32_t out_dtype, void* stream);
+
+/* Its gradient for the weights: dw[e][n][k] = sum over the rows r of e of dy[r][n] *
+ * x[src(r)][k]; dy [rows][N] and x [x_rows][K] in dtype, dw [E][N][K]. Every element is
+ * written: an expert without rows gets zeros (also with rows == 0, which may pass null dy
+ * and x). Errors as nvfp4_grouped_linear. */
+int nvfp4_grouped_linear_dw(const void* dy, const void* x, int32_t x_rows, int32_t dtype,
+                            const int32_t* expert_offsets, int32_t E, const int32_t* sorted_pairs, int32_t topk,
+                            int32_t rows, int32_t N, int32_t K, void* dw, int32_t out_dtype, void* stream);
+
+/* Combine of rows in the sorted order into their tokens: out[t][h] = sum over slots j, in
+ * order, of topk_weights[t][j] * y[pos][h], pos the row with sorted_pairs[pos] == t * topk +
+ * j; a dropped pair (in no row) adds nothing. topk_weights float [T][topk], or NULL for
+ * weights of 1. y [T*topk][H] in y_dtype, out [T][H] in out_dtype (fp32 sum, rounded once).
+ * ws needs nvfp4_moe_combine_workspace_size() bytes, any contents; calls sharing one must
+ * not overlap. T == 0 is a no-op. A pair listed twice (which nvfp4_moe_route never does)
+ * counts once.
+ * Errors: EINVAL for null or misaligned pointers (y, out, ws 16-byte aligned), T < 0,
+ * topk < 1, H < 1, unknown dtypes; EUNSUPPORTED for T * topk above 2^30, H above 2^20 or
+ * T * H of 2^38 or more; EWORKSPACE. */
+size_t nvfp4_moe_combine_workspace_size(int32_t T, int32_t topk);
+int nvfp4_moe_combine(const void* y, int32_t y_dtype, const int32_t* sorted_pairs, const float* topk_weights,
+                      int32_t T, int32_t topk, int32_t H, void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Its gradient: dy[pos][h] = topk_weights[t][j] * dout[t][h] (rounded once) and
+ * dweights[t][j] = sum_h dout[t][h] * y[pos][h] in fp32 (0 for a dropped pair). dout [T][H],
+ * y and dy [T*topk][H] in dtype; rows of dy that no pair has are left as they were.
+ * dweights may be NULL (then y may be too); topk_weights may be NULL (1). ws as above.
+ * Errors as nvfp4_moe_combine. */
+int nvfp4_moe_combine_grad(const void* dout, const void* y, int32_t dtype, const int32_t* sorted_pairs,
+                           const float* topk_weights, int32_t T, int32_t topk, int32_t H, void* dy, float* dweights,
+                           void* ws, size_t ws_bytes, void* stream);
+
 /* A static, human-readable name for a status code. */
 const char* nvfp4_status_string(int status);
 

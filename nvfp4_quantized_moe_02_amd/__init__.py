@@ -18,10 +18,18 @@ from .binding import (  # noqa: F401
     host_isa,
     moe_decode_host,
     Layer,
+    combine_workspace_size,
     dequant,
+    grouped_linear,
+    grouped_linear_dw,
+    grouped_linear_dx,
+    grouped_linear_i8,
     lib_path,
     linear,
+    linear_i8,
     load_library,
+    moe_combine,
+    moe_combine_grad,
     moe_decode,
     moe_decode_noalloc,
     moe_prefill,

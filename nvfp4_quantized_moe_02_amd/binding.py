@@ -111,6 +111,28 @@ _SIGS = {
                                 + [ctypes.POINTER(_Weight)] * 3 + [ctypes.c_int32] + [ctypes.POINTER(_Weight)] * 3
                                 + [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                    ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "nvfp4_linear_i8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.c_int32, ctypes.c_void_p]),
+    "nvfp4_grouped_linear_i8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
+                                + [ctypes.c_int32] * 4 + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "nvfp4_grouped_linear": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                            ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
+                             + [ctypes.c_int32] * 4 + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "nvfp4_grouped_linear_dx": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
+                                + [ctypes.c_int32] * 4 + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "nvfp4_grouped_linear_dw": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                               ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
+                                + [ctypes.c_int32] * 4 + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "nvfp4_moe_combine_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 2),
+    "nvfp4_moe_combine": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
+                          + [ctypes.c_int32] * 3 + [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                                    ctypes.c_size_t, ctypes.c_void_p]),
+    "nvfp4_moe_combine_grad": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                              ctypes.c_void_p] + [ctypes.c_int32] * 3
+                               + [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                  ctypes.c_void_p]),
 }
 
 
@@ -538,3 +560,200 @@ class PreparedHostCall:
     def run(self) -> int:
         _check("nvfp4_moe_decode_host", self.lib.nvfp4_moe_decode_host(*self.args))
         return int(self._dropped.value)
+
+
+# ---------------------------------------------------------------- 8- and 16-bit weights
+# These calls take caller-shaped tensors whose sizes the kernels index by, so shapes, dtypes
+# and devices are checked here; the device's stream is used with that device current.
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_device(dev: torch.device, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """One library call on dev's current stream, with dev the current device."""
+    _need(dev.type == "cuda", f"the library's device calls take GPU tensors (got {dev})")
+    f = getattr(load_library(), fn)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn, f(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, f(*args, _stream(dev)))
+
+
+def _out(out: Optional[torch.Tensor], shape, dtype: torch.dtype, dev: torch.device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(tuple(out.shape) == tuple(shape) and out.dtype in DTYPE, f"out must be a {tuple(shape)} library-dtype tensor")
+    _same_device(dev, out=out)
+    return out
+
+
+def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x int8 [T][K] with x_scale float32 [T] (as quant_rows_i8 gives them), w int8 [N][K]
+    with w_scale float32 [N]. Returns [T][N] in out_dtype (or out, in its own dtype)."""
+    _need(x.dim() == 2 and w.dim() == 2 and x.dtype == torch.int8 and w.dtype == torch.int8
+          and x.shape[1] == w.shape[1], "x and w must be int8 [T][K] and [N][K]")
+    T, K = x.shape
+    N = w.shape[0]
+    _need(x_scale.dtype == torch.float32 and x_scale.numel() == T and w_scale.dtype == torch.float32
+          and w_scale.numel() == N, "x_scale and w_scale must be float32 [T] and [N]")
+    dev = x.device
+    _same_device(dev, x_scale=x_scale, w=w, w_scale=w_scale)
+    out = _out(out, (T, N), out_dtype, dev)
+    _call("nvfp4_linear_i8", dev, _ptr(x), _ptr(x_scale), T, _ptr(w), _ptr(w_scale), N, K, _ptr(out),
+          DTYPE[out.dtype])
+    return out
+
+
+def _grouped_rows(x_rows: int, offsets: torch.Tensor, E: int, pairs: Optional[torch.Tensor], topk: int,
+                  dev: torch.device) -> int:
+    """Checks the routing of a grouped call; returns its number of sorted rows."""
+    _need(offsets.dtype == torch.int32 and offsets.numel() == E + 1, "expert_offsets must be int32 [E+1]")
+    _same_device(dev, expert_offsets=offsets)
+    if pairs is None:
+        return x_rows
+    _need(pairs.dtype == torch.int32 and pairs.dim() == 1 and topk >= 1 and pairs.numel() == x_rows * topk,
+          "sorted_pairs must be int32 [x_rows * topk]")
+    _same_device(dev, sorted_pairs=pairs)
+    return x_rows * topk
+
+
+def grouped_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                      expert_offsets: torch.Tensor, sorted_pairs: Optional[torch.Tensor] = None, topk: int = 1,
+                      out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """int8 experts w [E][N][K] with w_scale float32 [E][N] over rows sorted by expert (route).
+    x int8 [T][K] with x_scale float32 [T]: tokens when sorted_pairs is given (the product
+    gathers them), else rows in the sorted order. Returns [rows][N]; rows behind
+    expert_offsets[E] are left as they were (uninitialized in a new tensor)."""
+    _need(x.dim() == 2 and w.dim() == 3 and x.dtype == torch.int8 and w.dtype == torch.int8
+          and x.shape[1] == w.shape[2], "x and w must be int8 [T][K] and [E][N][K]")
+    T, K = x.shape
+    E, N = w.shape[0], w.shape[1]
+    _need(x_scale.dtype == torch.float32 and x_scale.numel() == T and w_scale.dtype == torch.float32
+          and tuple(w_scale.shape) == (E, N), "x_scale and w_scale must be float32 [T] and [E][N]")
+    dev = x.device
+    _same_device(dev, x_scale=x_scale, w=w, w_scale=w_scale)
+    rows = _grouped_rows(T, expert_offsets, E, sorted_pairs, topk, dev)
+    out = _out(out, (rows, N), out_dtype, dev)
+    _call("nvfp4_grouped_linear_i8", dev, _ptr(x), _ptr(x_scale), T, _ptr(w), _ptr(w_scale), _ptr(expert_offsets), E,
+          _ptr(sorted_pairs), topk, rows, N, K, _ptr(out), DTYPE[out.dtype])
+    return out
+
+
+def grouped_linear(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor,
+                   sorted_pairs: Optional[torch.Tensor] = None, topk: int = 1,
+                   out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Experts w [E][N][K] in bfloat16 or float16 over rows sorted by expert (route). x in the
+    same dtype: tokens [T][K] when sorted_pairs is given, else rows in the sorted order.
+    Returns [rows][N] (x's dtype by default); rows behind expert_offsets[E] are left as they
+    were (uninitialized in a new tensor)."""
+    _need(x.dim() == 2 and w.dim() == 3 and x.dtype in DTYPE and x.dtype == w.dtype and x.shape[1] == w.shape[2],
+          "x and w must be [T][K] and [E][N][K] of one library dtype")
+    T, K = x.shape
+    E, N = w.shape[0], w.shape[1]
+    dev = x.device
+    _same_device(dev, w=w)
+    rows = _grouped_rows(T, expert_offsets, E, sorted_pairs, topk, dev)
+    out = _out(out, (rows, N), out_dtype or x.dtype, dev)
+    _call("nvfp4_grouped_linear", dev, _ptr(x), T, _ptr(w), DTYPE[x.dtype], _ptr(expert_offsets), E,
+          _ptr(sorted_pairs), topk, rows, N, K, _ptr(out), DTYPE[out.dtype])
+    return out
+
+
+def grouped_linear_dx(dy: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor,
+                      out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of grouped_linear for its rows: dy [rows][N], w [E][N][K] -> dx [rows][K] in the
+    sorted order (sum a token's slots with moe_combine when x was gathered)."""
+    _need(dy.dim() == 2 and w.dim() == 3 and dy.dtype in DTYPE and dy.dtype == w.dtype
+          and dy.shape[1] == w.shape[1], "dy and w must be [rows][N] and [E][N][K] of one library dtype")
+    rows, N = dy.shape
+    E, K = w.shape[0], w.shape[2]
+    dev = dy.device
+    _same_device(dev, w=w)
+    _grouped_rows(rows, expert_offsets, E, None, 1, dev)
+    out = _out(out, (rows, K), out_dtype or dy.dtype, dev)
+    _call("nvfp4_grouped_linear_dx", dev, _ptr(dy), _ptr(w), DTYPE[dy.dtype], _ptr(expert_offsets), E, rows, N, K,
+          _ptr(out), DTYPE[out.dtype])
+    return out
+
+
+def grouped_linear_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch.Tensor,
+                      sorted_pairs: Optional[torch.Tensor] = None, topk: int = 1,
+                      out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of grouped_linear for its weights: dy [rows][N], x as in the forward call ->
+    dw [E][N][K] (zeros for an expert without rows)."""
+    _need(dy.dim() == 2 and x.dim() == 2 and dy.dtype in DTYPE and dy.dtype == x.dtype,
+          "dy and x must be [rows][N] and [T][K] of one library dtype")
+    T, K = x.shape
+    E, N = expert_offsets.numel() - 1, dy.shape[1]
+    dev = dy.device
+    _same_device(dev, x=x)
+    rows = _grouped_rows(T, expert_offsets, E, sorted_pairs, topk, dev)
+    _need(dy.shape[0] == rows, "dy must have one row per sorted row")
+    out = _out(out, (E, N, K), out_dtype or dy.dtype, dev)
+    _call("nvfp4_grouped_linear_dw", dev, _ptr(dy), _ptr(x), T, DTYPE[dy.dtype], _ptr(expert_offsets), E,
+          _ptr(sorted_pairs), topk, rows, N, K, _ptr(out), DTYPE[out.dtype])
+    return out
+
+
+def combine_workspace_size(T: int, topk: int) -> int:
+    return int(load_library().nvfp4_moe_combine_workspace_size(T, topk))
+
+
+def _combine_ws(ws: Optional[torch.Tensor], T: int, topk: int, dev: torch.device) -> torch.Tensor:
+    need = combine_workspace_size(T, topk)
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(ws.dtype == torch.uint8, "ws must be uint8")
+    _same_device(dev, ws=ws)
+    return ws
+
+
+def moe_combine(y: torch.Tensor, sorted_pairs: torch.Tensor, topk: int, w: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [T*topk][H] in the order of sorted_pairs -> [T][H], each token's rows times its router
+    weights w float32 [T][topk] (None: 1), summed in slot order. Dropped pairs add nothing."""
+    _need(y.dim() == 2 and y.dtype in DTYPE and sorted_pairs.dtype == torch.int32 and topk >= 1
+          and sorted_pairs.numel() == y.shape[0] and y.shape[0] % topk == 0,
+          "y must be [T*topk][H] and sorted_pairs int32 [T*topk]")
+    T, H = y.shape[0] // topk, y.shape[1]
+    _need(w is None or (w.dtype == torch.float32 and w.numel() == T * topk), "w must be float32 [T][topk]")
+    dev = y.device
+    _same_device(dev, sorted_pairs=sorted_pairs, w=w)
+    out = _out(out, (T, H), out_dtype or y.dtype, dev)
+    ws = _combine_ws(ws, T, topk, dev)
+    _call("nvfp4_moe_combine", dev, _ptr(y), DTYPE[y.dtype], _ptr(sorted_pairs), _ptr(w), T, topk, H, _ptr(out),
+          DTYPE[out.dtype], _ptr(ws), ws.numel())
+    return out
+
+
+def moe_combine_grad(dout: torch.Tensor, y: torch.Tensor, sorted_pairs: torch.Tensor, w: torch.Tensor,
+                     dy: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Gradients of moe_combine: (dy [T*topk][H] in y's dtype, dw float32 [T][topk]). Rows of dy
+    that no pair has are left as they were (uninitialized in a new tensor)."""
+    _need(dout.dim() == 2 and y.dim() == 2 and w.dim() == 2 and y.dtype in DTYPE and dout.dtype == y.dtype
+          and w.dtype == torch.float32 and dout.shape[1] == y.shape[1] and w.shape[0] == dout.shape[0]
+          and y.shape[0] == w.numel(), "dout [T][H], y [T*topk][H] of one library dtype, w float32 [T][topk]")
+    _need(sorted_pairs.dtype == torch.int32 and sorted_pairs.numel() == y.shape[0],
+          "sorted_pairs must be int32 [T*topk]")
+    T, H = dout.shape
+    topk = w.shape[1]
+    dev = y.device
+    _same_device(dev, dout=dout, sorted_pairs=sorted_pairs, w=w)
+    dy = _out(dy, tuple(y.shape), y.dtype, dev)
+    _need(dy.dtype == y.dtype, "dy must have y's dtype")
+    dw = torch.empty_like(w)
+    ws = _combine_ws(ws, T, topk, dev)
+    _call("nvfp4_moe_combine_grad", dev, _ptr(dout), _ptr(y), DTYPE[y.dtype], _ptr(sorted_pairs), _ptr(w), T, topk, H,
+          _ptr(dy), _ptr(dw), _ptr(ws), ws.numel())
+    return dy, dw
