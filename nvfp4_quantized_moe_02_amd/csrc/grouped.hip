@@ -8,10 +8,12 @@
 //   dw       dw_e[n][k]  = sum_{r of e} dy[r][n] x[src r][k]
 //
 // All three are C[m][c] = sum_j A[m][j] B[c][j]. An operand whose contraction index j is
-// contiguous in memory (x and w forward, dy in dx) is staged as LDS rows of 64 bytes of j;
-// the others (w in dx, both in dw) as 32 rows of j, each a run of m or c, and read
+// contiguous in memory (x and w forward, dy in dx) is staged as LDS rows of JB bytes of j;
+// the others (w in dx, both in dw) as JB / 2 rows of j, each a run of m or c, and read
 // through the LDS transpose load. 64 bytes are 32 sixteen-bit or 64 eight-bit values: two
 // matrix instructions of 32 x 32 outputs either way, with the same 16 bytes per lane.
+#include <type_traits>
+
 #include "grouped.h"
 
 namespace nvfp4 {
@@ -22,8 +24,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kFwd = 0, kDx = 1, kDw = 2;
 constexpr int kBf16 = 0, kF16 = 1, kI8 = 2;
-constexpr int JB = 64;        // bytes of the contraction dimension per K-block
-constexpr int JR = 32;        // contraction rows per K-block of a transposed operand
 constexpr int kIdxTile = 1024;  // rows of the gather table of dw
 
 typedef __attribute__((address_space(3))) char* lds_char_t;
@@ -32,10 +32,21 @@ typedef __attribute__((address_space(3))) char* lds_char_t;
 // In asm because the compiler waits for every outstanding load before any LDS read that
 // might alias the builtin's LDS write; the waits are wait_barrier's. The instruction
 // writes no register.
-__device__ __forceinline__ void dma16(const void* src, const char* dst) {
-  const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char_t)dst);
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(m) : "memory", "m0");
+// The address is a scalar base (one per K-block) and a 32-bit offset per lane; gathered rows
+// take a whole address per lane.
+__device__ __forceinline__ void dma16(const char* base, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst)
+               : "memory", "m0");
 }
+__device__ __forceinline__ void dma16(const char* addr, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(addr), "s"(dst)
+               : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_addr(const char* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char_t)p);
+}
+// a value that is the same in every lane, for the scalar unit
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // At most N vector loads of this wave outstanding, its LDS reads done, then the barrier.
 template <int N>
@@ -49,6 +60,9 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+
+// Nothing is scheduled across: the loads and fragment reads stay where they are written.
+__device__ __forceinline__ void hold_order() { __builtin_amdgcn_sched_barrier(0); }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
@@ -131,11 +145,11 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int bm, int NB, 
     }
   }
   __syncthreads();
-  t.e = s_tile[0];
-  t.base = s_tile[1];
+  t.e = uni(s_tile[0]);
+  t.base = uni(s_tile[1]);
   t.m0 = 0;
-  t.rows = s_tile[2];
-  t.nb = (int)(L - (long long)mt * NB);
+  t.rows = uni(s_tile[2]);
+  t.nb = uni((int)(L - (long long)mt * NB));
   return t.rows > 0;  // 0: offsets that do not ascend, whose counts disagree
 }
 
@@ -173,36 +187,17 @@ __device__ __forceinline__ typename Acc<T>::v16 mma16(i32x4_t a, i32x4_t b, type
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-// Four adjacent outputs of one row, rounded once to the output type. n: columns left in
-// the row (fewer than 4 only in the last group); vec: the row's groups of 4 are aligned.
-__device__ __forceinline__ void store4(void* out, int dtype, size_t at, const float* v, int n, bool vec) {
-  if (n <= 0) return;
-  if (dtype == 0) {
-    float* o = reinterpret_cast<float*>(out) + at;
-    if (vec && n >= 4)
-      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      for (int j = 0; j < 4; ++j)
-        if (j < n) o[j] = v[j];
-  } else {
-    uint16_t* o = reinterpret_cast<uint16_t*>(out) + at;
-    uint32_t h[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = dtype == 1 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
-    if (vec && n >= 4)
-      *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-    else
-      for (int j = 0; j < 4; ++j)
-        if (j < n) o[j] = (uint16_t)h[j];
-  }
-}
-
 // ------------------------------------------------------------------ LDS images of a K-block
-// Straight operand: rows of 64 bytes, 16-byte chunk c of row r in slot c ^ ((r >> 2) & 3):
-// the 16 rows that an LDS read cycle serves then cover all 64 banks once.
-__device__ __forceinline__ int straight_at(int row, int chunk) { return row * JB + ((chunk ^ ((row >> 2) & 3)) << 4); }
+// Straight operand: rows of JB bytes, 16-byte chunk c of row r in slot c ^ key(r): the 16
+// rows that an LDS read cycle serves then cover all 64 banks once (measured: no conflicts).
+template <int JB>
+struct Straight {
+  static constexpr int CPR = JB / 16;
+  __device__ static int key(int row) { return JB == 64 ? (row >> 2) & 3 : (row >> 1) & 7; }
+  __device__ static int at(int row, int chunk) { return row * JB + ((chunk ^ key(row)) << 4); }
+};
 
-// Transposed operand: 32 contraction rows of W elements (2 W bytes). A transpose load
+// Transposed operand: JB / 2 contraction rows of W elements (2 W bytes). A transpose load
 // takes 4 rows x 64 bytes per 32 lanes; the 64-byte blocks of a row are permuted by the
 // row so that those four rows fall on different banks.
 template <int W>
@@ -214,119 +209,217 @@ struct Trans {
   __device__ static int key(int row) { return (row / PER) & MASK; }
 };
 
-template <int OP, int T, int WM, int WN, int RB, int CB, int ST>
+template <int OP, int T, int WM, int WN, int RB, int CB, int JB, int ST>
 struct Cfg {
   static constexpr int BM = WM * RB * 32, BN = WN * CB * 32, THREADS = WM * WN * 64;
   static constexpr bool ATR = OP == kDw, BTR = OP != kFwd;
   static constexpr int ABYTES = BM * JB, BBYTES = BN * JB, STAGE = ABYTES + BBYTES;
-  static constexpr int NLA = BM * 4 / THREADS, NLB = BN * 4 / THREADS;
-  static_assert(BM * 4 % THREADS == 0 && BN * 4 % THREADS == 0, "whole loads per thread");
+  static constexpr int NLA = ABYTES / 16 / THREADS, NLB = BBYTES / 16 / THREADS;
+  static_assert(ST * STAGE / (WM * WN) >= 32 * (CB * 128 + 16), "room for the epilogue");
+  static_assert(ABYTES / 16 % THREADS == 0 && BBYTES / 16 % THREADS == 0, "whole loads per thread");
 };
 
-// The tile's K loop and epilogue for NRB occupied row blocks per wave (NRB < RB only when
-// one wave row covers the tile).
-template <int OP, int T, int WM, int WN, int RB, int CB, int ST, int NRB>
+// Stores a wave's NRB x CB blocks of 32 x 32 outputs of OS bytes each, one row block at a
+// time through `buf` (wave-private LDS). value(rb, cb, i, scale) is accumulator element i;
+// rows first .. of the tile below mlim exist, as do columns below nout.
+template <int OS, int CB, int NRB, bool ALIGNED, class V, class S>
+__device__ __forceinline__ void store_rows(const GroupedArgs& g, char* buf, V value, S scale, int first, int mlim,
+                                           size_t out0, int col0, int nout) {
+  const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+  constexpr int PITCH = CB * 32 * OS + 16;
+  constexpr int CPR = CB * 32 * OS / 16;  // 16-byte chunks per row
+  constexpr int E = 16 / OS;              // outputs per chunk
+  char* out = reinterpret_cast<char*>(g.out);
+  const bool vec = ALIGNED || nout % E == 0;
+  const int ch = lane % CPR, r0 = lane / CPR;
+  const int col = col0 + ch * E;
+#pragma unroll
+  for (int rb = 0; rb < NRB; ++rb) {
+    const float rs = scale(rb);
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = value(rb, cb, 4 * q + j, rs);
+        char* p = buf + l32 * PITCH + (cb * 32 + 8 * q + 4 * half) * OS;
+        if constexpr (OS == 4) {
+          *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+          uint32_t h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = g.out_dtype == 1 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
+          *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        }
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the other lanes' rows are in LDS
+#pragma unroll
+    for (int i = 0; i < CPR / 2; ++i) {
+      const int r = r0 + i * (64 / CPR), row = first + rb * 32 + r;
+      const uint4 v = *reinterpret_cast<const uint4*>(buf + r * PITCH + ch * 16);
+      if (row < mlim && col < nout) {
+        char* p = out + ((out0 + row) * nout + col) * OS;
+        if (vec) {
+          *reinterpret_cast<uint4*>(p) = v;
+        } else {
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (col + j < nout) {
+              if constexpr (OS == 4)
+                reinterpret_cast<uint32_t*>(p)[j] = u[j];
+              else
+                reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(u[j / 2] >> (16 * (j & 1)));
+            }
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next row block overwrites
+  }
+}
+
+// The tile's K loop and epilogue for NRB occupied row blocks of this wave (0 .. RB).
+//
+// Every K-block is KS steps of 32 bytes of the contraction. A step's fragments are read while
+// the step before multiplies. The last step of a K-block starts with the one barrier: by
+// then every wave holds that K-block's last fragments, so its stage may be refilled, and the
+// next K-block's loads have arrived, so its first fragments are read under the last step's
+// matrix instructions. The refill's loads are issued one at a time between them: in one burst
+// they queue in the address unit ahead of the wave's next instructions.
+template <int OP, int T, int WM, int WN, int RB, int CB, int JB, int ST, int NRB>
 __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int base, int mrows, int m0, int c0, int C,
                                              char* lds, int* s_src) {
-  typedef Cfg<OP, T, WM, WN, RB, CB, ST> F;
+  typedef Cfg<OP, T, WM, WN, RB, CB, JB, ST> F;
   constexpr int ES = T == kI8 ? 1 : 2;
   constexpr int THREADS = F::THREADS;
-  // loads of A: only the occupied row blocks when the rows are straight
-  constexpr int NA = F::ATR ? F::NLA : (WM * NRB * 32 * 4 + THREADS - 1) / THREADS;
+  // loads of A: only the occupied row blocks when one row of waves covers the straight tile
+  constexpr int NA = F::ATR || WM > 1 ? F::NLA : (NRB * 32 * (JB / 16) + THREADS - 1) / THREADS;
   constexpr int NBL = F::NLB;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int LPS = NA + NBL;  // loads per stage and thread
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int half = lane >> 5, l32 = lane & 31;
   const int nout = OP == kFwd ? g.N : g.K;  // columns of C
-  const int mlim = OP == kDw ? g.N : mrows;  // rows of C in this tile's range
+  const int mlim = OP == kDw ? g.N - m0 : mrows;  // rows of C from the tile's first
   constexpr int JE = JB / ES;               // contraction elements per K-block
+  constexpr int JR = JB / 2;                // contraction rows per K-block of a transposed operand
+  constexpr int KS = JB / 32;               // matrix-instruction steps per K-block
+  typedef Straight<JB> SX;
   const int nk = (C + JE - 1) / JE;
   const int tail = C - (nk - 1) * JE;       // elements of the last K-block
 
-  // ---- where this thread's chunks come from
+  // ---- where this thread's chunks come from: scalar bases that move with the K-blocks and
+  // offsets from them (below 2^32: a tile is at most 256 rows of 2^20 values); rows of x that
+  // may be gathered (forward A, dw's B) have 64-bit addresses
+  constexpr bool AG = OP == kFwd;
+  const char* abase = reinterpret_cast<const char*>(g.a);
+  const char* bbase = reinterpret_cast<const char*>(g.b);
+  uint32_t ao[NA], bo[NBL];
   const char* ap[NA];
-  const char* bp[NBL];
   int arow[NA], brow[NBL], ach[NA], bch[NBL];
+  const size_t astep = F::ATR ? (size_t)JR * g.N * 2 : JB, bstep = F::BTR ? (size_t)JR * g.K * 2 : JB;
+  if constexpr (F::ATR)
+    abase += ((size_t)base * g.N + m0) * 2;
+  else if constexpr (OP == kDx)
+    abase += (size_t)base * g.N * ES;
+  if constexpr (OP == kFwd)
+    bbase += ((size_t)e * g.N + c0) * g.K * ES;
+  else if constexpr (OP == kDx)
+    bbase += ((size_t)e * g.N * g.K + c0) * 2;
+  else
+    bbase += (size_t)c0 * 2;
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
     const int ci = i * THREADS + tid;
     if constexpr (!F::ATR) {
-      arow[i] = ci >> 2;
-      ach[i] = ((ci & 3) ^ ((arow[i] >> 2) & 3));
-      const int lda = OP == kFwd ? g.K : g.N;
+      arow[i] = ci / SX::CPR;
+      ach[i] = (ci % SX::CPR) ^ SX::key(arow[i]);
       const int r = arow[i] < mrows ? arow[i] : mrows - 1;
-      const size_t sr = OP == kFwd ? (size_t)s_src[r] : (size_t)(base + r);
-      ap[i] = reinterpret_cast<const char*>(g.a) + sr * lda * ES;
+      if constexpr (AG)
+        ap[i] = abase + (size_t)s_src[r] * g.K * ES + ach[i] * 16;
+      else
+        ao[i] = r * (uint32_t)(g.N * ES) + ach[i] * 16;
     } else {
       typedef Trans<F::BM> X;
       arow[i] = ci / X::CPR;
       const int s = ci % X::CPR;
       const int ch = (((s >> 2) ^ X::key(arow[i])) << 2) | (s & 3);
-      const int col = m0 + ch * 8 < g.N ? m0 + ch * 8 : 0;
       ach[i] = 0;
-      ap[i] = reinterpret_cast<const char*>(g.a) + (size_t)col * 2;
+      ao[i] = (arow[i] * (uint32_t)g.N + (m0 + ch * 8 < g.N ? ch * 8 : 0)) * 2;
     }
   }
 #pragma unroll
   for (int i = 0; i < NBL; ++i) {
     const int ci = i * THREADS + tid;
     if constexpr (!F::BTR) {
-      brow[i] = ci >> 2;
-      bch[i] = ((ci & 3) ^ ((brow[i] >> 2) & 3));
-      const int n = c0 + brow[i] < g.N ? c0 + brow[i] : g.N - 1;
-      bp[i] = reinterpret_cast<const char*>(g.b) + ((size_t)e * g.N + n) * g.K * ES;
+      brow[i] = ci / SX::CPR;
+      bch[i] = (ci % SX::CPR) ^ SX::key(brow[i]);
+      const int n = c0 + brow[i] < g.N ? brow[i] : g.N - 1 - c0;
+      bo[i] = n * (uint32_t)(g.K * ES) + bch[i] * 16;
     } else {
       typedef Trans<F::BN> X;
       brow[i] = ci / X::CPR;
       const int s = ci % X::CPR;
       const int ch = (((s >> 2) ^ X::key(brow[i])) << 2) | (s & 3);
-      const int col = c0 + ch * 8 < g.K ? c0 + ch * 8 : 0;
       bch[i] = 0;
-      const size_t first = OP == kDx ? (size_t)e * g.N * g.K : 0;
-      bp[i] = reinterpret_cast<const char*>(g.b) + (first + col) * 2;
+      // dw: the row comes from the table; bo is the column only
+      bo[i] = ((OP == kDx ? brow[i] * (uint32_t)g.K : 0) + (c0 + ch * 8 < g.K ? ch * 8 : 0)) * 2;
     }
   }
-  // K-block kb into stage s. Chunks and rows past the contraction's end read something in
-  // bounds; zero_tail clears them in LDS.
-  auto issue = [&](int kb, int s) {
-    char* As = lds + s * F::STAGE;
-    char* Bs = As + F::ABYTES;
-    const bool last = kb == nk - 1;
-    if (OP == kDw && g.pairs != nullptr && (kb % (kIdxTile / JR)) == 0) {
-      // the next kIdxTile rows' source rows (kb is the same in every wave)
-      lds_barrier();
-      for (int r = tid; r < kIdxTile; r += THREADS) {
-        const int j = kb * JR + r;
-        s_src[r] = j < C ? src_row(g, base + j) : 0;
-      }
-      lds_barrier();
-    }
+  // Before the loads of K-block kb: in the last one, chunks and rows past the contraction's
+  // end read something in bounds (zero_tail clears them in LDS); dw's table of source rows
+  // is refilled every kIdxTile rows (a barrier: kb is the same in every wave, and every
+  // wave has passed a barrier since its last look at the table).
+  auto prepare = [&](int kb) {
+    if (kb == nk - 1 && tail < JE) {
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const char* p;
-      if constexpr (!F::ATR) {
-        const int off = kb * JB + ach[i] * 16;
-        p = ap[i] + (last && off >= C * ES ? 0 : off);
-      } else {
-        const int j = kb * JR + arow[i];
-        p = ap[i] + (size_t)(base + (j < C ? j : C - 1)) * g.N * 2;
+      for (int i = 0; i < NA; ++i) {
+        if constexpr (F::ATR)
+          ao[i] -= arow[i] >= tail ? (arow[i] - (tail - 1)) * (uint32_t)g.N * 2 : 0;
+        else if constexpr (AG)
+          ap[i] -= ach[i] * (16 / ES) >= tail ? ach[i] * 16 : 0;
+        else
+          ao[i] -= ach[i] * (16 / ES) >= tail ? ach[i] * 16 : 0;
       }
-      dma16(p, As + (i * THREADS + wave * 64) * 16);
-    }
+      if constexpr (OP != kDw) {
 #pragma unroll
-    for (int i = 0; i < NBL; ++i) {
-      const char* p;
-      if constexpr (!F::BTR) {
-        const int off = kb * JB + bch[i] * 16;
-        p = bp[i] + (last && off >= C * ES ? 0 : off);
-      } else {
-        int j = kb * JR + brow[i];
-        j = j < C ? j : C - 1;
-        size_t r = j;
-        if (OP == kDw) r = g.pairs != nullptr ? s_src[j % kIdxTile] : base + j;
-        p = bp[i] + r * g.K * 2;
+        for (int i = 0; i < NBL; ++i) {
+          if constexpr (F::BTR)
+            bo[i] -= brow[i] >= tail ? (brow[i] - (tail - 1)) * (uint32_t)g.K * 2 : 0;
+          else
+            bo[i] -= bch[i] * (16 / ES) >= tail ? bch[i] * 16 : 0;
+        }
       }
-      dma16(p, Bs + (i * THREADS + wave * 64) * 16);
+    }
+    if constexpr (OP == kDw) {
+      if (kb % (kIdxTile / JR) == 0) {
+        for (int r = tid; r < kIdxTile; r += THREADS) {
+          const int j = kb * JR + r;
+          s_src[r] = src_row(g, base + (j < C ? j : C - 1));
+        }
+        lds_barrier();
+      }
+    }
+  };
+  const uint32_t lds0 = lds_addr(lds) + wave * 1024;
+  // load i of K-block kb into stage s (in order; prepare(kb) first)
+  auto issue = [&](int kb, int s, int i) {
+    const uint32_t dst = lds0 + s * F::STAGE + i * THREADS * 16;
+    if (i < NA) {
+      if constexpr (AG) {
+        dma16(ap[i], dst);
+        ap[i] += JB;
+      } else {
+        dma16(abase + kb * astep, ao[i], dst);
+      }
+    } else {
+      const int b = i - NA;
+      const uint32_t d = dst + (F::NLA - NA) * THREADS * 16;
+      if constexpr (OP == kDw)
+        dma16(bbase + (size_t)s_src[(kb * JR + brow[b]) % kIdxTile] * (g.K * 2) + bo[b], d);
+      else
+        dma16(bbase + kb * bstep, bo[b], d);
     }
   };
   auto zero_tail = [&](int s) {
@@ -341,10 +434,11 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
     for (int i = 0; i < NBL; ++i)
       if (F::BTR ? brow[i] >= tail : bch[i] * (16 / ES) >= tail)
         *reinterpret_cast<uint4*>(Bs + (i * THREADS + tid) * 16) = z;
+    lds_barrier();
   };
   // fragment of operand block `blk` (32 rows of m or c), K-step ks
   auto frag_straight = [&](const char* S, int row, int ks) -> i32x4_t {
-    return *reinterpret_cast<const i32x4_t*>(S + straight_at(row, 2 * ks + half));
+    return *reinterpret_cast<const i32x4_t*>(S + SX::at(row, 2 * ks + half));
   };
   const int tr_row = 8 * half + ((lane & 15) >> 2);
   const int tr_in = (16 * ((lane >> 4) & 1) + 4 * (lane & 3)) * 2;
@@ -361,88 +455,159 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
     return __builtin_bit_cast(i32x4_t, __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
-  typename Acc<T>::v32 acc[NRB][CB];
+  constexpr int R = NRB > 0 ? NRB : 1;
+  typename Acc<T>::v32 acc[R][CB];
 #pragma unroll
-  for (int rb = 0; rb < NRB; ++rb)
+  for (int rb = 0; rb < R; ++rb)
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[rb][cb][i] = 0;
-
-  constexpr int LPS = NA + NBL;  // loads per stage and thread
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s)
-    if (s < nk) issue(s, s);
-  int cur = 0;
-  for (int kb = 0; kb < nk; ++kb) {
-    // stage kb has arrived when at most the later stages' loads are outstanding
-    if (kb + ST - 2 < nk)
-      wait_barrier<LPS*(ST - 2)>();
-    else
-      wait_barrier<0>();
-    const int nxt = cur == 0 ? ST - 1 : cur - 1;  // (kb + ST - 1) % ST
-    if (kb + ST - 1 < nk) issue(kb + ST - 1, nxt);
-    if (kb == nk - 1 && tail < JE) {
-      zero_tail(cur);
-      lds_barrier();
-    }
-    const char* As = lds + cur * F::STAGE;
-    const char* Bs = As + F::ABYTES;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      i32x4_t bf[CB];
+  i32x4_t fa[2][R], fb[2][CB];
+  auto read_frags = [&](int s, int ks, int q) {
+    if constexpr (NRB > 0) {
+      const char* As = lds + s * F::STAGE;
+      const char* Bs = As + F::ABYTES;
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) {
         if constexpr (F::BTR)
-          bf[cb] = frag_trans(Bs, Trans<F::BN>{}, wn * CB + cb, ks);
+          fb[q][cb] = frag_trans(Bs, Trans<F::BN>{}, wn * CB + cb, ks);
         else
-          bf[cb] = frag_straight(Bs, (wn * CB + cb) * 32 + l32, ks);
+          fb[q][cb] = frag_straight(Bs, (wn * CB + cb) * 32 + l32, ks);
       }
 #pragma unroll
       for (int rb = 0; rb < NRB; ++rb) {
-        i32x4_t af;
         if constexpr (F::ATR)
-          af = frag_trans(As, Trans<F::BM>{}, wm * RB + rb, ks);
+          fa[q][rb] = frag_trans(As, Trans<F::BM>{}, wm * RB + rb, ks);
         else
-          af = frag_straight(As, (wm * RB + rb) * 32 + l32, ks);
-        // columns first: a lane ends with 4 x 4 adjacent columns of one row
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = mma32<T>(bf[cb], af, acc[rb][cb]);
+          fa[q][rb] = frag_straight(As, (wm * RB + rb) * 32 + l32, ks);
       }
     }
-    cur = cur + 1 == ST ? 0 : cur + 1;
+  };
+  // step ks's matrix instructions, with share `slot` of the loads of K-block `fill` between
+  constexpr int PER = (LPS + KS - 1) / KS;
+  auto multiply = [&](int ks, auto filling, int slot, int fill, int fstage) {
+#pragma unroll
+    for (int rb = 0; rb < R; ++rb) {
+      if constexpr (NRB > 0) {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = mma32<T>(fb[ks & 1][cb], fa[ks & 1][rb], acc[rb][cb]);
+      }
+      if constexpr (decltype(filling)::value) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i * R / PER == rb && slot * PER + i < LPS) {
+            issue(fill, fstage, slot * PER + i);
+            hold_order();
+          }
+      }
+    }
+  };
+
+  if (nk > 0) {
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+      if (s < nk) {
+        prepare(s);
+#pragma unroll
+        for (int i = 0; i < LPS; ++i) issue(s, s, i);
+      }
+    if (nk >= ST)
+      wait_barrier<LPS*(ST - 1)>();
+    else
+      wait_barrier<0>();
+    if (nk == 1 && tail < JE) zero_tail(0);
+    read_frags(0, 0, 0);
+#pragma unroll
+    for (int ks = 0; ks + 1 < KS; ++ks) {
+      read_frags(0, ks + 1, (ks + 1) & 1);
+      multiply(ks, std::false_type{}, 0, 0, 0);
+    }
+  }
+  int cur = 0, kb = 0;
+  // the last step of K-block kb, the others of kb + 1, and the loads of kb + ST
+  for (; kb + ST < nk; ++kb) {
+    const int nxt = cur + 1 == ST ? 0 : cur + 1;
+    wait_barrier<LPS*(ST - 2)>();
+    read_frags(nxt, 0, 0);
+    prepare(kb + ST);
+    hold_order();
+    multiply(KS - 1, std::true_type{}, 0, kb + ST, cur);
+#pragma unroll
+    for (int ks = 0; ks + 1 < KS; ++ks) {
+      read_frags(nxt, ks + 1, (ks + 1) & 1);
+      hold_order();
+      multiply(ks, std::true_type{}, ks + 1, kb + ST, cur);
+    }
+    cur = nxt;
+  }
+  for (; kb < nk; ++kb) {
+    const int nxt = cur + 1 == ST ? 0 : cur + 1;
+    const int later = nk - 2 - kb;  // K-blocks behind the next one, all being loaded
+    if (later >= 0) {
+      if (ST > 3 && later >= 2)
+        wait_barrier<LPS*(ST > 3 ? 2 : 0)>();
+      else if (ST > 2 && later == 1)
+        wait_barrier<LPS*(ST > 2 ? 1 : 0)>();
+      else
+        wait_barrier<0>();
+      if (later == 0 && tail < JE) zero_tail(nxt);
+      read_frags(nxt, 0, 0);
+    }
+    multiply(KS - 1, std::false_type{}, 0, 0, 0);
+    if (later >= 0) {
+#pragma unroll
+      for (int ks = 0; ks + 1 < KS; ++ks) {
+        read_frags(nxt, ks + 1, (ks + 1) & 1);
+        multiply(ks, std::false_type{}, 0, 0, 0);
+      }
+    }
+    cur = nxt;
   }
 
   // Accumulator element i of lane (half, l32): row l32 of the row block, column
-  // 8 (i / 4) + 4 half + i % 4 of the column block.
-  const bool vec = (nout & 3) == 0;
+  // 8 (i / 4) + 4 half + i % 4 of the column block. Each wave passes a row block through its
+  // part of the stages, so that it stores whole runs of a row (128 bytes of 16-bit outputs)
+  // instead of 8 bytes per row.
+  lds_barrier();
+  if constexpr (NRB > 0) {
+    char* mine = lds + wave * (ST * F::STAGE / (WM * WN));
+    const int col0 = c0 + wn * CB * 32;
+    float bs[CB][4][4];
+    if constexpr (T == kI8) {
 #pragma unroll
-  for (int rb = 0; rb < NRB; ++rb) {
-    const int m = (wm * RB + rb) * 32 + l32;
-    const int row = OP == kDw ? m0 + m : m;
-    if (row >= mlim) continue;
-    const size_t at = (OP == kDw ? (size_t)e * g.N + row : (size_t)(base + row)) * nout;
-    float rs = 1.f;
-    if constexpr (T == kI8) rs = g.a_scale[s_src[row]];
+      for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = c0 + (wn * CB + cb) * 32 + 8 * q + 4 * half;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = (float)acc[rb][cb][4 * q + j];
-          if constexpr (T == kI8) v[j] = v[j] * rs * (col + j < nout ? g.b_scale[(size_t)e * g.N + col + j] : 0.f);
-        }
-        store4(g.out, g.out_dtype, at + col, v, nout - col, vec);
+          for (int j = 0; j < 4; ++j) {
+            const int col = col0 + cb * 32 + 8 * q + 4 * half + j;
+            bs[cb][q][j] = g.b_scale[(size_t)e * g.N + (col < g.N ? col : g.N - 1)];
+          }
+    }
+    const size_t out0 = OP == kDw ? (size_t)e * g.N + m0 : (size_t)base;
+    auto value = [&](int rb, int cb, int i, float rs) -> float {
+      float v = (float)acc[rb][cb][i];
+      if constexpr (T == kI8) {
+        v = v * rs * bs[cb][i >> 2][i & 3];
+        // the output is this fp32 value rounded again: kept apart from the narrowing, which the
+        // backend would fold into one mixed-precision multiply
+        asm volatile("" : "+v"(v));
       }
+      return v;
+    };
+    if (g.out_dtype == 0)
+      store_rows<4, CB, NRB, OP != kFwd || T != kI8>(
+          g, mine, value, [&](int rb) { return T == kI8 ? g.a_scale[s_src[(wm * RB + rb) * 32 + l32]] : 1.f; }, wm * RB * 32, mlim, out0, col0, nout);
+    else
+      store_rows<2, CB, NRB, OP != kFwd || T != kI8>(
+          g, mine, value, [&](int rb) { return T == kI8 ? g.a_scale[s_src[(wm * RB + rb) * 32 + l32]] : 1.f; }, wm * RB * 32, mlim, out0, col0, nout);
   }
 }
 
-template <int OP, int T, int WM, int WN, int RB, int CB, int ST>
+template <int OP, int T, int WM, int WN, int RB, int CB, int JB, int ST>
 __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, int NB) {
-  typedef Cfg<OP, T, WM, WN, RB, CB, ST> F;
+  typedef Cfg<OP, T, WM, WN, RB, CB, JB, ST> F;
   __shared__ __attribute__((aligned(256))) char lds[ST * F::STAGE];
   __shared__ int s_src[OP == kDw ? kIdxTile : F::BM];
   if constexpr (OP == kDw) {
@@ -451,11 +616,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, 
     const long long total = (long long)g.E * NM * NB, per = (total + 7) >> 3;
     const long long L = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     if ((long long)(blockIdx.x >> 3) >= per || L >= total) return;
-    const int e = (int)(L / (NM * NB)), rest = (int)(L - (long long)e * NM * NB);
+    const int e = uni((int)(L / (NM * NB))), rest = uni((int)(L - (long long)e * NM * NB));
     const int mb = rest / NB, nb = rest - mb * NB;
-    const int lo = clampi(g.offsets[e], 0, g.P), hi = clampi(g.offsets[e + 1], lo, g.P);
+    const int lo = uni(clampi(g.offsets[e], 0, g.P)), hi = uni(clampi(g.offsets[e + 1], lo, g.P));
     // an expert without rows has a zero gradient: no K-block, the cleared accumulator is stored
-    tile_product<OP, T, WM, WN, RB, CB, ST, RB>(g, e, lo, 0, mb * F::BM, nb * F::BN, hi - lo, lds, s_src);
+    tile_product<OP, T, WM, WN, RB, CB, JB, ST, RB>(g, e, lo, 0, mb * F::BM, nb * F::BN, hi - lo, lds, s_src);
   } else {
     Tile t;
     if (!find_tile<F::THREADS>(g, F::BM, NB, t)) return;
@@ -466,18 +631,22 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, 
       __syncthreads();
     }
     const int c0 = t.nb * F::BN, C = OP == kFwd ? g.K : g.N;
-    if constexpr (WM == 1 && RB == 4) {
-      const int nrb = (t.rows + 31) >> 5;
+    if constexpr (RB == 4) {
+      // occupied row blocks of this wave's row of waves (the same in all its lanes)
+      const int nrb = __builtin_amdgcn_readfirstlane(
+          clampi(((t.rows + 31) >> 5) - (int)(threadIdx.x >> 6) / WN * RB, 0, RB));
       if (nrb == 4)
-        tile_product<OP, T, WM, WN, RB, CB, ST, 4>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
+        tile_product<OP, T, WM, WN, RB, CB, JB, ST, 4>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
       else if (nrb == 3)
-        tile_product<OP, T, WM, WN, RB, CB, ST, 3>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
+        tile_product<OP, T, WM, WN, RB, CB, JB, ST, 3>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
       else if (nrb == 2)
-        tile_product<OP, T, WM, WN, RB, CB, ST, 2>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
+        tile_product<OP, T, WM, WN, RB, CB, JB, ST, 2>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
+      else if (WM > 1 && nrb == 0)
+        tile_product<OP, T, WM, WN, RB, CB, JB, ST, WM == 1>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
       else
-        tile_product<OP, T, WM, WN, RB, CB, ST, 1>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
+        tile_product<OP, T, WM, WN, RB, CB, JB, ST, 1>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
     } else {
-      tile_product<OP, T, WM, WN, RB, CB, ST, RB>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
+      tile_product<OP, T, WM, WN, RB, CB, JB, ST, RB>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
     }
   }
 }
@@ -489,9 +658,9 @@ static unsigned grid_rows(const GroupedArgs& g, int bm, int NB) {
   return (unsigned)((tiles * NB + 7) / 8 * 8);
 }
 
-template <int OP, int T, int WM, int WN, int RB, int CB, int ST>
+template <int OP, int T, int WM, int WN, int RB, int CB, int JB, int ST>
 static hipError_t launch_cfg(const GroupedArgs& g, hipStream_t st) {
-  typedef Cfg<OP, T, WM, WN, RB, CB, ST> F;
+  typedef Cfg<OP, T, WM, WN, RB, CB, JB, ST> F;
   const int nout = OP == kFwd ? g.N : g.K;
   const int NB = (nout + F::BN - 1) / F::BN;
   unsigned grid;
@@ -499,26 +668,47 @@ static hipError_t launch_cfg(const GroupedArgs& g, hipStream_t st) {
     grid = (unsigned)(((long long)g.E * ((g.N + F::BM - 1) / F::BM) * NB + 7) / 8 * 8);
   else
     grid = grid_rows(g, F::BM, NB);
-  grouped_kernel<OP, T, WM, WN, RB, CB, ST><<<grid, F::THREADS, 0, st>>>(g, NB);
+  grouped_kernel<OP, T, WM, WN, RB, CB, JB, ST><<<grid, F::THREADS, 0, st>>>(g, NB);
   return hipGetLastError();
+}
+
+// Two tiles. 256 x 256 by 8 waves (one block per CU, four 64-byte stages) reads half as much
+// per product as 128 x 256 by 4 waves (two blocks per CU, three stages), which leaves less of a
+// tile empty at the end of an expert and overlaps one block's stores with the other's
+// products. Measured (2048 -> 1536, top 8 of 8192 tokens): forward with 1024 rows per expert
+// 437 against 472 us, with 128 rows 846 against 839; dx 454 / 435 and 829 / 760; dw 564 / 592
+// and 1427 / 1495; dense int8 8192 x 4096 x 4096 135 / 147 us; int8 down with 128 rows
+// 350 / 282.
+template <int OP, int T>
+static hipError_t launch_tiles(const GroupedArgs& g, bool big, hipStream_t st) {
+  if (big) return launch_cfg<OP, T, 2, 4, 4, 2, 64, 4>(g, st);
+  return launch_cfg<OP, T, 1, 4, 4, 2, 64, 3>(g, st);
+}
+
+// rows an expert has on average, of those that can have any
+static int64_t rows_per_expert(const GroupedArgs& g) {
+  const int64_t e = g.offsets == nullptr ? 1 : (g.E < g.P ? g.E : g.P);
+  return e > 0 ? g.P / e : 0;
 }
 
 hipError_t launch_grouped_fwd(int type, const GroupedArgs& g, hipStream_t st) {
   if (g.P == 0) return hipSuccess;
-  if (type == kBf16) return launch_cfg<kFwd, kBf16, 1, 4, 4, 2, 3>(g, st);
-  if (type == kF16) return launch_cfg<kFwd, kF16, 1, 4, 4, 2, 3>(g, st);
-  return launch_cfg<kFwd, kI8, 1, 4, 4, 2, 3>(g, st);
+  const bool big = rows_per_expert(g) >= 512;
+  if (type == kBf16) return launch_tiles<kFwd, kBf16>(g, big, st);
+  if (type == kF16) return launch_tiles<kFwd, kF16>(g, big, st);
+  return launch_tiles<kFwd, kI8>(g, big, st);
 }
 
 hipError_t launch_grouped_dx(int type, const GroupedArgs& g, hipStream_t st) {
   if (g.P == 0) return hipSuccess;
-  if (type == kBf16) return launch_cfg<kDx, kBf16, 1, 4, 4, 2, 3>(g, st);
-  return launch_cfg<kDx, kF16, 1, 4, 4, 2, 3>(g, st);
+  if (type == kBf16) return launch_tiles<kDx, kBf16>(g, false, st);
+  return launch_tiles<kDx, kF16>(g, false, st);
 }
 
 hipError_t launch_grouped_dw(int type, const GroupedArgs& g, hipStream_t st) {
-  if (type == kBf16) return launch_cfg<kDw, kBf16, 1, 4, 4, 2, 3>(g, st);
-  return launch_cfg<kDw, kF16, 1, 4, 4, 2, 3>(g, st);
+  const bool big = (int64_t)g.N * g.K >= 256 * 256;
+  if (type == kBf16) return launch_tiles<kDw, kBf16>(g, big, st);
+  return launch_tiles<kDw, kF16>(g, big, st);
 }
 
 }  // namespace nvfp4
