@@ -74,29 +74,32 @@ __device__ __forceinline__ int src_row(const GroupedArgs& g, int r) {
 }
 
 struct Tile {
-  int e, m0, rows, base, nb;
+  int e, rows, base, nb;  // the tile's rows are base .. base + rows - 1
 };
 
-// The expert and row tile of this block: row tiles of bm rows in expert order, the NB
-// column blocks of a row tile one after the other. Each XCD (blockIdx % 8) takes a
-// contiguous range, so the column blocks that share rows of x and the row tiles that share
-// weights meet in one L2. Every block sums the tile counts itself from the offsets (one
-// round trip and one block scan), so no launch before this one has to build a list.
-// Offsets are clamped to [0, P]. Returns false for a block without a tile.
+// Row tiles are counted in expert order (an expert with n rows has ceil(n / bm)), and every row
+// tile has NB column blocks, one after the other. Each XCD (blockIdx % 8) takes a contiguous
+// range of these blocks, so that those that share rows of x and those that share weights meet
+// in one L2. Offsets are clamped to [0, P].
+
+//
+// Every block finds its tile from the offsets itself (one round trip and one block scan), so
+// that no launch and no workspace comes before this one; a launch that lists the tiles gained
+// 1 to 4% where there are 1000 tiles. Ranges even in cost rather than in blocks (a first row
+// tile, which brings an expert's weights from memory, counted twice) lost 5%. Returns false
+// for a block without a tile.
 template <int THREADS>
 __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int bm, int NB, Tile& t) {
   __shared__ int s_tot[THREADS / 64];
   __shared__ int s_tile[3];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int bid = blockIdx.x;
-  const int xcd = bid & 7, jj = bid >> 3;
-  int mt;
+  const int xcd = blockIdx.x & 7, jj = blockIdx.x >> 3;
   if (g.offsets == nullptr) {
-    const int total = ((g.P + bm - 1) / bm) * NB, per = (total + 7) >> 3;
-    const int L = xcd * per + jj;
+    const long long total = (long long)((g.P + bm - 1) / bm) * NB, per = (total + 7) >> 3;
+    const long long L = xcd * per + jj;
     if (jj >= per || L >= total) return false;
-    mt = L / NB;
-    t = Tile{0, mt * bm, g.P - mt * bm < bm ? g.P - mt * bm : bm, 0, L - mt * NB};
+    const int mt = (int)(L / NB);
+    t = Tile{0, g.P - mt * bm < bm ? g.P - mt * bm : bm, mt * bm, (int)(L - (long long)mt * NB)};
     return true;
   }
   const int per_t = (g.E + THREADS - 1) / THREADS;
@@ -126,7 +129,7 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int bm, int NB, 
   const long long total = (long long)tiles * NB, per = (total + 7) >> 3;
   const long long L = xcd * per + jj;
   if (jj >= per || L >= total) return false;
-  mt = (int)(L / NB);
+  const int mt = (int)(L / NB);
   int excl = before + inc - cnt;
   if (mt >= excl && mt < excl + cnt) {
     lo = clampi(g.offsets[e0], 0, g.P);
@@ -147,7 +150,6 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int bm, int NB, 
   __syncthreads();
   t.e = uni(s_tile[0]);
   t.base = uni(s_tile[1]);
-  t.m0 = 0;
   t.rows = uni(s_tile[2]);
   t.nb = uni((int)(L - (long long)mt * NB));
   return t.rows > 0;  // 0: offsets that do not ascend, whose counts disagree
@@ -611,50 +613,175 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, 
   __shared__ __attribute__((aligned(256))) char lds[ST * F::STAGE];
   __shared__ int s_src[OP == kDw ? kIdxTile : F::BM];
   if constexpr (OP == kDw) {
-    // blocks of (expert, BM rows n, BN columns k); an XCD takes a contiguous range
-    const int NM = (g.N + F::BM - 1) / F::BM;
-    const long long total = (long long)g.E * NM * NB, per = (total + 7) >> 3;
-    const long long L = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((long long)(blockIdx.x >> 3) >= per || L >= total) return;
-    const int e = uni((int)(L / (NM * NB))), rest = uni((int)(L - (long long)e * NM * NB));
-    const int mb = rest / NB, nb = rest - mb * NB;
+    // Every XCD takes an eighth of each expert's tiles (BM rows n, BN columns k), so experts
+    // with many rows do not gather on one; which eighth turns with the expert.
+    const int tiles = (g.N + F::BM - 1) / F::BM * NB, per = (tiles + 7) >> 3;
+    const int j = blockIdx.x >> 3;
+    const int e = j / per, tile = ((blockIdx.x + e) & 7) * per + (j - e * per);
+    if (tile >= tiles) return;
+    const int mb = tile / NB, nb = tile - mb * NB;
     const int lo = uni(clampi(g.offsets[e], 0, g.P)), hi = uni(clampi(g.offsets[e + 1], lo, g.P));
     // an expert without rows has a zero gradient: no K-block, the cleared accumulator is stored
     tile_product<OP, T, WM, WN, RB, CB, JB, ST, RB>(g, e, lo, 0, mb * F::BM, nb * F::BN, hi - lo, lds, s_src);
   } else {
     Tile t;
     if (!find_tile<F::THREADS>(g, F::BM, NB, t)) return;
-    const int base = t.base + t.m0;
+    const int base = t.base;
     if constexpr (OP == kFwd) {
       for (int r = threadIdx.x; r < F::BM; r += F::THREADS)
         s_src[r] = src_row(g, base + (r < t.rows ? r : t.rows - 1));
       __syncthreads();
     }
     const int c0 = t.nb * F::BN, C = OP == kFwd ? g.K : g.N;
-    if constexpr (RB == 4) {
-      // occupied row blocks of this wave's row of waves (the same in all its lanes)
-      const int nrb = __builtin_amdgcn_readfirstlane(
-          clampi(((t.rows + 31) >> 5) - (int)(threadIdx.x >> 6) / WN * RB, 0, RB));
-      if (nrb == 4)
-        tile_product<OP, T, WM, WN, RB, CB, JB, ST, 4>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
-      else if (nrb == 3)
-        tile_product<OP, T, WM, WN, RB, CB, JB, ST, 3>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
-      else if (nrb == 2)
-        tile_product<OP, T, WM, WN, RB, CB, JB, ST, 2>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
-      else if (WM > 1 && nrb == 0)
-        tile_product<OP, T, WM, WN, RB, CB, JB, ST, WM == 1>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
-      else
-        tile_product<OP, T, WM, WN, RB, CB, JB, ST, 1>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
-    } else {
-      tile_product<OP, T, WM, WN, RB, CB, JB, ST, RB>(g, t.e, base, t.rows, 0, c0, C, lds, s_src);
-    }
+    // occupied row blocks of this wave's row of waves (the same in all its lanes)
+    const int nrb = uni(clampi(((t.rows + 31) >> 5) - (int)(threadIdx.x >> 6) / WN * RB, 0, RB));
+#define NVFP4_TILE(NRB) tile_product<OP, T, WM, WN, RB, CB, JB, ST, NRB>(g, t.e, base, t.rows, 0, c0, C, lds, s_src)
+    if (nrb == RB)
+      NVFP4_TILE(RB);
+    else if (RB > 3 && nrb == 3)
+      NVFP4_TILE((RB > 3 ? 3 : RB));
+    else if (RB > 2 && nrb == 2)
+      NVFP4_TILE((RB > 2 ? 2 : RB));
+    else if (WM > 1 && nrb == 0)
+      NVFP4_TILE((WM > 1 ? 0 : RB));
+    else
+      NVFP4_TILE(1);
+#undef NVFP4_TILE
   }
 }
 
-// Blocks for the most row tiles that P rows in E experts can make.
+// ------------------------------------------------------------------ few rows
+// Four adjacent outputs of one row, rounded once to the output type. n: columns left in
+// the row (fewer than 4 only in the last group); vec: the row's groups of 4 are aligned.
+__device__ __forceinline__ void store4(void* out, int dtype, size_t at, const float* v, int n, bool vec) {
+  if (n <= 0) return;
+  if (dtype == 0) {
+    float* o = reinterpret_cast<float*>(out) + at;
+    if (vec && n >= 4)
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      for (int j = 0; j < 4; ++j)
+        if (j < n) o[j] = v[j];
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(out) + at;
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = dtype == 1 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
+    if (vec && n >= 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    else
+      for (int j = 0; j < 4; ++j)
+        if (j < n) o[j] = (uint16_t)h[j];
+  }
+}
+
+// Forward product of up to 16 RB rows: bound by reading the weights once. A block takes 16 NW
+// weight rows of one expert; its four waves split the contraction, each reading U
+// consecutive 64-byte steps of its rows straight into registers (U (NW + RB) loads of 16
+// bytes per lane in flight) and multiplying them on 16 x 16 matrix instructions, the weights as
+// the first operand. The four partial results are added in wave order through LDS.
+template <int T, int RB, int U, int NW>
+__global__ __launch_bounds__(256) void stream_kernel(GroupedArgs g, int NB) {
+  constexpr int ES = T == kI8 ? 1 : 2;
+  typedef typename Acc<T>::v16 V;
+  __shared__ V s_part[4][NW * RB][64];
+  Tile t;
+  if (!find_tile<256>(g, 16 * RB, NB, t)) return;
+  const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
+  const int l16 = lane & 15, ch = lane >> 4;
+  const int base = t.base;
+  const int n0 = t.nb * 16 * NW;
+  const int kb = g.K * ES;  // bytes of a row
+  const char* wp[NW];
+  const char* xp[RB];
+  int src[RB];
+#pragma unroll
+  for (int q = 0; q < NW; ++q) {
+    const int n = n0 + q * 16 + l16 < g.N ? n0 + q * 16 + l16 : g.N - 1;
+    wp[q] = reinterpret_cast<const char*>(g.b) + ((size_t)t.e * g.N + n) * kb + ch * 16;
+  }
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int r = rb * 16 + l16;
+    src[rb] = src_row(g, base + (r < t.rows ? r : t.rows - 1));
+    xp[rb] = reinterpret_cast<const char*>(g.a) + (size_t)src[rb] * kb + ch * 16;
+  }
+  V acc[NW][RB];
+#pragma unroll
+  for (int q = 0; q < NW; ++q)
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[q][rb][i] = 0;
+  for (int s0 = wave * U; s0 * 64 < kb; s0 += 4 * U) {
+    i32x4_t w[NW][U], x[RB][U];
+    const int at = s0 * 64;
+    if (at + U * 64 <= kb) {
+#pragma unroll
+      for (int q = 0; q < NW; ++q)
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[q][u] = *reinterpret_cast<const i32x4_t*>(wp[q] + at + u * 64);
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[rb][u] = *reinterpret_cast<const i32x4_t*>(xp[rb] + at + u * 64);
+    } else {
+      // the row's end: chunks past it are zero in both operands
+      const i32x4_t z = {0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = at + u * 64 + ch * 16 < kb;
+#pragma unroll
+        for (int q = 0; q < NW; ++q) w[q][u] = in ? *reinterpret_cast<const i32x4_t*>(wp[q] + at + u * 64) : z;
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) x[rb][u] = in ? *reinterpret_cast<const i32x4_t*>(xp[rb] + at + u * 64) : z;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < NW; ++q)
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) acc[q][rb] = mma16<T>(w[q][u], x[rb][u], acc[q][rb]);
+  }
+#pragma unroll
+  for (int q = 0; q < NW; ++q)
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) s_part[wave][q * RB + rb][lane] = acc[q][rb];
+  __syncthreads();
+  // wave w finishes block w of the NW x RB: lane (ch, l16) has row l16 and columns 4 ch ..
+#pragma unroll
+  for (int q = 0; q < NW; ++q)
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      if (q * RB + rb != wave) continue;
+      const int r = rb * 16 + l16;
+      if (r >= t.rows) continue;
+      V sum = s_part[0][q * RB + rb][lane];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) sum += s_part[w][q * RB + rb][lane];
+      const int col = n0 + q * 16 + 4 * ch;
+      float v[4];
+      float rs = 1.f;
+      if constexpr (T == kI8) rs = g.a_scale[src[rb]];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = (float)sum[j];
+        if constexpr (T == kI8) {
+          v[j] = v[j] * rs * g.b_scale[(size_t)t.e * g.N + (col + j < g.N ? col + j : g.N - 1)];
+          asm volatile("" : "+v"(v[j]));  // rounded to fp32 before the output type, as in tile_product
+        }
+      }
+      store4(g.out, g.out_dtype, (size_t)(base + r) * g.N + col, v, g.N - col, (g.N & 3) == 0);
+    }
+}
+
+// The most row tiles that P rows in E experts can make.
+static long long most_tiles(int P, int E, int bm) { return P / bm + (E < P ? E : P); }
+
+// Blocks of a grid whose blocks find their tiles.
 static unsigned grid_rows(const GroupedArgs& g, int bm, int NB) {
-  const long long e = g.offsets == nullptr ? 1 : (g.E < g.P ? g.E : g.P);
-  const long long tiles = g.offsets == nullptr ? ((long long)g.P + bm - 1) / bm : g.P / bm + e;
+  const long long tiles = g.offsets == nullptr ? ((long long)g.P + bm - 1) / bm : most_tiles(g.P, g.E, bm);
   return (unsigned)((tiles * NB + 7) / 8 * 8);
 }
 
@@ -665,50 +792,94 @@ static hipError_t launch_cfg(const GroupedArgs& g, hipStream_t st) {
   const int NB = (nout + F::BN - 1) / F::BN;
   unsigned grid;
   if (OP == kDw)
-    grid = (unsigned)(((long long)g.E * ((g.N + F::BM - 1) / F::BM) * NB + 7) / 8 * 8);
+    grid = (unsigned)((long long)g.E * (((g.N + F::BM - 1) / F::BM * NB + 7) / 8) * 8);
   else
     grid = grid_rows(g, F::BM, NB);
   grouped_kernel<OP, T, WM, WN, RB, CB, JB, ST><<<grid, F::THREADS, 0, st>>>(g, NB);
   return hipGetLastError();
 }
 
-// Two tiles. 256 x 256 by 8 waves (one block per CU, four 64-byte stages) reads half as much
-// per product as 128 x 256 by 4 waves (two blocks per CU, three stages), which leaves less of a
-// tile empty at the end of an expert and overlaps one block's stores with the other's
-// products. Measured (2048 -> 1536, top 8 of 8192 tokens): forward with 1024 rows per expert
-// 437 against 472 us, with 128 rows 846 against 839; dx 454 / 435 and 829 / 760; dw 564 / 592
-// and 1427 / 1495; dense int8 8192 x 4096 x 4096 135 / 147 us; int8 down with 128 rows
-// 350 / 282.
-template <int OP, int T>
-static hipError_t launch_tiles(const GroupedArgs& g, bool big, hipStream_t st) {
-  if (big) return launch_cfg<OP, T, 2, 4, 4, 2, 64, 4>(g, st);
-  return launch_cfg<OP, T, 1, 4, 4, 2, 64, 3>(g, st);
+template <int T, int RB, int U, int NW>
+static hipError_t launch_stream(const GroupedArgs& g, hipStream_t st) {
+  static_assert(NW * RB <= 4, "one wave finishes each block");
+  const int NB = (g.N + 16 * NW - 1) / (16 * NW);
+  stream_kernel<T, RB, U, NW><<<grid_rows(g, 16 * RB, NB), 256, 0, st>>>(g, NB);
+  return hipGetLastError();
 }
 
-// rows an expert has on average, of those that can have any
-static int64_t rows_per_expert(const GroupedArgs& g) {
-  const int64_t e = g.offsets == nullptr ? 1 : (g.E < g.P ? g.E : g.P);
-  return e > 0 ? g.P / e : 0;
+// Rows of an expert when all experts that can have rows have the same, and the row tiles of bm
+// rows that this makes.
+struct Load {
+  int64_t experts, rows;
+  explicit Load(const GroupedArgs& g) {
+    experts = g.offsets == nullptr ? 1 : (g.E < g.P ? g.E : g.P);
+    rows = (g.P + experts - 1) / experts;
+  }
+  int64_t tiles(int bm) const { return experts * ((rows + bm - 1) / bm); }
+};
+static int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
+
+// The largest tile that still fills the device, because a larger tile reads less per product:
+//   256 x 256, 8 waves, one block per CU, four 64-byte stages
+//   128 x 256, 4 waves, two blocks per CU, three stages: less of a tile is empty at the end
+//     of an expert, and one block's stores overlap the other's products
+//   64 x 128, 4 waves, two blocks per CU, three 128-byte stages
+//   64 x 64, 4 waves, four 128-byte stages
+// Measured, us (top 8, 2048 -> 1536 in bf16 unless said): 64 experts, 8192 tokens, forward
+// 256 x 256 437, 128 x 256 472, 64 x 128 600; dx 440 / 435 / 670; 8 experts, forward 117 /
+// 132 / 155; 512 experts, uniform, 32 rows each: 128 x 256 595, 64 x 128 588; 64 rows each
+// 648 / 714; dx of 8 rows each 459 / 479. Dense int8 2048 x 4096 x 4096 (256 tiles of
+// 128 x 256): 45, 64 x 128 72; 1024 rows (128 tiles): 38 / 36, 64 x 64 42; 512 rows 34 / 24 /
+// 23; 128 rows 33 / 15 / 11.
+template <int OP, int T>
+static hipError_t launch_tiles(const GroupedArgs& g, const Load& l, hipStream_t st) {
+  const int nout = OP == kFwd ? g.N : g.K;
+  const int64_t t128 = l.tiles(128) * blocks(nout, 256);
+  if (l.rows >= (OP == kFwd ? 512 : 1024) && l.tiles(256) * blocks(nout, 256) >= 256)
+    return launch_cfg<OP, T, 2, 4, 4, 2, 64, 4>(g, st);
+  if (t128 >= 192 && (OP == kDx || l.rows >= 48)) return launch_cfg<OP, T, 1, 4, 4, 2, 64, 3>(g, st);
+  if (l.tiles(64) * blocks(nout, 128) >= 300) return launch_cfg<OP, T, 1, 4, 2, 1, 128, 3>(g, st);
+  return launch_cfg<OP, T, 2, 2, 1, 1, 128, 4>(g, st);
+}
+
+template <int T>
+static hipError_t forward(const GroupedArgs& g, hipStream_t st) {
+  const Load l(g);
+  const int64_t n16 = blocks(g.N, 16), row_kb = (int64_t)g.K * (T == kI8 ? 1 : 2);
+  // Few rows: the weights stream. Dense int8 4096 x 4096, 1 row: 6.7 us, 64 x 64 tile 10.1; 512
+  // experts in bf16, 8 rows: 13.3 / 12.8, 16 rows: two groups of weight rows 21.9, one 23.8, tile
+  // 24.2; 64 rows 53.6 / 56.0 / 58.7. Past 16 rows each row tile reads the weights again, which
+  // pays while that is little: dense int8 1001 x 1040, 128 rows: 4.8, tile 7.7; 2048 x 2048, 64
+  // rows 6.7 / 7.8, 128 rows 9.5 / 8.1.
+  if (l.rows <= 16 && g.P <= 64)
+    return l.tiles(16) * n16 >= 1536 ? launch_stream<T, 1, 8, 2>(g, st) : launch_stream<T, 1, 8, 1>(g, st);
+  if (l.tiles(32) * n16 * row_kb <= 640 * 1024) return launch_stream<T, 2, 4, 1>(g, st);
+  return launch_tiles<kFwd, T>(g, l, st);
 }
 
 hipError_t launch_grouped_fwd(int type, const GroupedArgs& g, hipStream_t st) {
   if (g.P == 0) return hipSuccess;
-  const bool big = rows_per_expert(g) >= 512;
-  if (type == kBf16) return launch_tiles<kFwd, kBf16>(g, big, st);
-  if (type == kF16) return launch_tiles<kFwd, kF16>(g, big, st);
-  return launch_tiles<kFwd, kI8>(g, big, st);
+  if (type == kBf16) return forward<kBf16>(g, st);
+  if (type == kF16) return forward<kF16>(g, st);
+  return forward<kI8>(g, st);
 }
 
 hipError_t launch_grouped_dx(int type, const GroupedArgs& g, hipStream_t st) {
   if (g.P == 0) return hipSuccess;
-  if (type == kBf16) return launch_tiles<kDx, kBf16>(g, false, st);
-  return launch_tiles<kDx, kF16>(g, false, st);
+  if (type == kBf16) return launch_tiles<kDx, kBf16>(g, Load(g), st);
+  return launch_tiles<kDx, kF16>(g, Load(g), st);
+}
+
+template <int T>
+static hipError_t weight_gradient(const GroupedArgs& g, hipStream_t st) {
+  // 256 x 256 while that fills the device: 64 experts of 1536 x 2048, 8192 tokens 472 us, 128 x 128
+  // 526; 13 experts of 520 x 392 (78 tiles) 20.0, 128 x 128 12.5
+  if (g.E * blocks(g.N, 256) * blocks(g.K, 256) >= 256) return launch_cfg<kDw, T, 2, 4, 4, 2, 64, 4>(g, st);
+  return launch_cfg<kDw, T, 2, 2, 2, 2, 64, 3>(g, st);
 }
 
 hipError_t launch_grouped_dw(int type, const GroupedArgs& g, hipStream_t st) {
-  const bool big = (int64_t)g.N * g.K >= 256 * 256;
-  if (type == kBf16) return launch_tiles<kDw, kBf16>(g, big, st);
-  return launch_tiles<kDw, kF16>(g, big, st);
+  return type == kBf16 ? weight_gradient<kBf16>(g, st) : weight_gradient<kF16>(g, st);
 }
 
 }  // namespace nvfp4
