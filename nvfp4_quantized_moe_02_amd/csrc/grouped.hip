@@ -167,7 +167,7 @@ struct Acc<kI8> {
 };
 
 template <int T>
-__device__ __forceinline__ typename Acc<T>::v32 mma32(i32x4_t a, i32x4_t b, typename Acc<T>::v32 c) {
+__device__ __forceinline__ typename Acc<T>::v32 mma(i32x4_t a, i32x4_t b, typename Acc<T>::v32 c) {
   if constexpr (T == kBf16)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
@@ -178,7 +178,7 @@ __device__ __forceinline__ typename Acc<T>::v32 mma32(i32x4_t a, i32x4_t b, type
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
 }
 template <int T>
-__device__ __forceinline__ typename Acc<T>::v16 mma16(i32x4_t a, i32x4_t b, typename Acc<T>::v16 c) {
+__device__ __forceinline__ typename Acc<T>::v16 mma(i32x4_t a, i32x4_t b, typename Acc<T>::v16 c) {
   if constexpr (T == kBf16)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
@@ -211,23 +211,26 @@ struct Trans {
   __device__ static int key(int row) { return (row / PER) & MASK; }
 };
 
-template <int OP, int T, int WM, int WN, int RB, int CB, int JB, int ST>
+template <int OP, int T, int WM, int WN, int RB, int CB, int MT, int JB, int ST>
 struct Cfg {
   static constexpr int BM = WM * RB * 32, BN = WN * CB * 32, THREADS = WM * WN * 64;
   static constexpr bool ATR = OP == kDw, BTR = OP != kFwd;
   static constexpr int ABYTES = BM * JB, BBYTES = BN * JB, STAGE = ABYTES + BBYTES;
   static constexpr int NLA = ABYTES / 16 / THREADS, NLB = BBYTES / 16 / THREADS;
   static_assert(ST * STAGE / (WM * WN) >= 32 * (CB * 128 + 16), "room for the epilogue");
+  static_assert(MT == 32 || OP == kFwd, "transposed operands are read for 32 x 32");
+  static_assert(JB >= 128 || MT == 32, "two steps per K-block at least");
   static_assert(ABYTES / 16 % THREADS == 0 && BBYTES / 16 % THREADS == 0, "whole loads per thread");
 };
 
 // Stores a wave's NRB x CB blocks of 32 x 32 outputs of OS bytes each, one row block at a
 // time through `buf` (wave-private LDS). value(rb, cb, i, scale) is accumulator element i;
 // rows first .. of the tile below mlim exist, as do columns below nout.
-template <int OS, int CB, int NRB, bool ALIGNED, class V, class S>
+template <int OS, int MT, int CB, int NRB, bool ALIGNED, class V, class S>
 __device__ __forceinline__ void store_rows(const GroupedArgs& g, char* buf, V value, S scale, int first, int mlim,
                                            size_t out0, int col0, int nout) {
-  const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+  const int lane = threadIdx.x & 63, part = lane / MT, lm = lane % MT;
+  constexpr int U = 32 / MT, Q = MT == 32 ? 4 : 1;  // blocks per 32, runs of 4 columns per block and lane
   constexpr int PITCH = CB * 32 * OS + 16;
   constexpr int CPR = CB * 32 * OS / 16;  // 16-byte chunks per row
   constexpr int E = 16 / OS;              // outputs per chunk
@@ -237,24 +240,27 @@ __device__ __forceinline__ void store_rows(const GroupedArgs& g, char* buf, V va
   const int col = col0 + ch * E;
 #pragma unroll
   for (int rb = 0; rb < NRB; ++rb) {
-    const float rs = scale(rb);
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
+    for (int u = 0; u < U; ++u) {
+      const float rs = scale(rb * U + u);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[4];
+      for (int cb = 0; cb < CB * U; ++cb)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = value(rb, cb, 4 * q + j, rs);
-        char* p = buf + l32 * PITCH + (cb * 32 + 8 * q + 4 * half) * OS;
-        if constexpr (OS == 4) {
-          *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-          uint32_t h[4];
+        for (int q = 0; q < Q; ++q) {
+          float v[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = g.out_dtype == 1 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
-          *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+          for (int j = 0; j < 4; ++j) v[j] = value(rb * U + u, cb, 4 * q + j, rs);
+          char* p = buf + (u * MT + lm) * PITCH + (cb * MT + 8 * q + 4 * part) * OS;
+          if constexpr (OS == 4) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = g.out_dtype == 1 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
+            *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+          }
         }
-      }
+    }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the other lanes' rows are in LDS
 #pragma unroll
     for (int i = 0; i < CPR / 2; ++i) {
@@ -283,16 +289,17 @@ __device__ __forceinline__ void store_rows(const GroupedArgs& g, char* buf, V va
 
 // The tile's K loop and epilogue for NRB occupied row blocks of this wave (0 .. RB).
 //
-// Every K-block is KS steps of 32 bytes of the contraction. A step's fragments are read while
+// Every K-block is KS steps of 32 bytes of the contraction (64 for 16 x 16 matrix
+// instructions, MT 16). A step's fragments are read while
 // the step before multiplies. The last step of a K-block starts with the one barrier: by
 // then every wave holds that K-block's last fragments, so its stage may be refilled, and the
 // next K-block's loads have arrived, so its first fragments are read under the last step's
 // matrix instructions. The refill's loads are issued one at a time between them: in one burst
 // they queue in the address unit ahead of the wave's next instructions.
-template <int OP, int T, int WM, int WN, int RB, int CB, int JB, int ST, int NRB>
+template <int OP, int T, int WM, int WN, int RB, int CB, int MT, int JB, int ST, int NRB>
 __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int base, int mrows, int m0, int c0, int C,
                                              char* lds, int* s_src) {
-  typedef Cfg<OP, T, WM, WN, RB, CB, JB, ST> F;
+  typedef Cfg<OP, T, WM, WN, RB, CB, MT, JB, ST> F;
   constexpr int ES = T == kI8 ? 1 : 2;
   constexpr int THREADS = F::THREADS;
   // loads of A: only the occupied row blocks when one row of waves covers the straight tile
@@ -301,12 +308,13 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
   constexpr int LPS = NA + NBL;  // loads per stage and thread
   const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int half = lane >> 5, l32 = lane & 31;
+  const int part = lane / MT, lm = lane % MT;
   const int nout = OP == kFwd ? g.N : g.K;  // columns of C
   const int mlim = OP == kDw ? g.N - m0 : mrows;  // rows of C from the tile's first
   constexpr int JE = JB / ES;               // contraction elements per K-block
   constexpr int JR = JB / 2;                // contraction rows per K-block of a transposed operand
-  constexpr int KS = JB / 32;               // matrix-instruction steps per K-block
+  constexpr int SB = MT == 32 ? 32 : 64;    // bytes of the contraction per matrix instruction
+  constexpr int KS = JB / SB;               // matrix-instruction steps per K-block
   typedef Straight<JB> SX;
   const int nk = (C + JE - 1) / JE;
   const int tail = C - (nk - 1) * JE;       // elements of the last K-block
@@ -438,11 +446,12 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
         *reinterpret_cast<uint4*>(Bs + (i * THREADS + tid) * 16) = z;
     lds_barrier();
   };
-  // fragment of operand block `blk` (32 rows of m or c), K-step ks
-  auto frag_straight = [&](const char* S, int row, int ks) -> i32x4_t {
-    return *reinterpret_cast<const i32x4_t*>(S + SX::at(row, 2 * ks + half));
+  // fragment of operand block `blk` (MT rows of m or c), step ks: lane (part, lm) has 16 bytes of
+  // row lm
+  auto frag_straight = [&](const char* S, int blk, int ks) -> i32x4_t {
+    return *reinterpret_cast<const i32x4_t*>(S + SX::at(blk * MT + lm, ks * (SB / 16) + part));
   };
-  const int tr_row = 8 * half + ((lane & 15) >> 2);
+  const int tr_row = 8 * part + ((lane & 15) >> 2);
   const int tr_in = (16 * ((lane >> 4) & 1) + 4 * (lane & 3)) * 2;
   auto frag_trans = [&](const char* S, auto x, int blk, int ks) -> i32x4_t {
     typedef decltype(x) X;
@@ -457,34 +466,39 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
     return __builtin_bit_cast(i32x4_t, __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
-  constexpr int R = NRB > 0 ? NRB : 1;
-  typename Acc<T>::v32 acc[R][CB];
+  constexpr int U = 32 / MT;           // instructions' blocks per 32 rows or columns
+  constexpr int RM = NRB * U, CM = CB * U;
+  constexpr int R = RM > 0 ? RM : 1;
+  constexpr int AV = MT == 32 ? 16 : 4;  // accumulator elements per lane and block
+  typedef typename std::conditional<MT == 32, typename Acc<T>::v32, typename Acc<T>::v16>::type AccV;
+  AccV acc[R][CM];
 #pragma unroll
   for (int rb = 0; rb < R; ++rb)
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
+    for (int cb = 0; cb < CM; ++cb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[rb][cb][i] = 0;
-  i32x4_t fa[2][R], fb[2][CB];
-  auto read_frags = [&](int s, int ks, int q) {
-    if constexpr (NRB > 0) {
-      const char* As = lds + s * F::STAGE;
-      const char* Bs = As + F::ABYTES;
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        if constexpr (F::BTR)
-          fb[q][cb] = frag_trans(Bs, Trans<F::BN>{}, wn * CB + cb, ks);
-        else
-          fb[q][cb] = frag_straight(Bs, (wn * CB + cb) * 32 + l32, ks);
-      }
-#pragma unroll
-      for (int rb = 0; rb < NRB; ++rb) {
-        if constexpr (F::ATR)
-          fa[q][rb] = frag_trans(As, Trans<F::BM>{}, wm * RB + rb, ks);
-        else
-          fa[q][rb] = frag_straight(As, (wm * RB + rb) * 32 + l32, ks);
-      }
+      for (int i = 0; i < AV; ++i) acc[rb][cb][i] = 0;
+  i32x4_t fa[2][R], fb[2][CM];
+  // fragment f of step ks of stage s into set q: the CM of B, then the RM of A
+  auto read_frag = [&](int s, int ks, int q, int f) {
+    const char* As = lds + s * F::STAGE;
+    const char* Bs = As + F::ABYTES;
+    if (f < CM) {
+      if constexpr (F::BTR)
+        fb[q][f] = frag_trans(Bs, Trans<F::BN>{}, wn * CM + f, ks);
+      else
+        fb[q][f] = frag_straight(Bs, wn * CM + f, ks);
+    } else {
+      if constexpr (F::ATR)
+        fa[q][f - CM] = frag_trans(As, Trans<F::BM>{}, wm * RB * U + f - CM, ks);
+      else
+        fa[q][f - CM] = frag_straight(As, wm * RB * U + f - CM, ks);
     }
+  };
+  constexpr int NF = NRB > 0 ? CM + RM : 0;
+  auto read_frags = [&](int s, int ks, int q) {
+#pragma unroll
+    for (int f = 0; f < NF; ++f) read_frag(s, ks, q, f);
   };
   // step ks's matrix instructions, with share `slot` of the loads of K-block `fill` between
   constexpr int PER = (LPS + KS - 1) / KS;
@@ -493,7 +507,9 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
     for (int rb = 0; rb < R; ++rb) {
       if constexpr (NRB > 0) {
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) acc[rb][cb] = mma32<T>(fb[ks & 1][cb], fa[ks & 1][rb], acc[rb][cb]);
+        for (int cb = 0; cb < CM; ++cb) {
+          acc[rb][cb] = mma<T>(fb[ks & 1][cb], fa[ks & 1][rb], acc[rb][cb]);
+        }
       }
       if constexpr (decltype(filling)::value) {
 #pragma unroll
@@ -504,6 +520,30 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
           }
       }
     }
+  };
+
+  // The same with one fragment of the next step (rs, rks) read before each matrix instruction
+  // instead of all of them ahead of the step (16 x 16 instructions, of which a step has 2 to 3
+  // times as many as fragments).
+  auto interleaved = [&](int ks, int rs, int rks, int slot, int fill, int fstage) {
+    constexpr int NM = RM * CM, SL = NM > 0 ? NM : 1;
+    constexpr int RPS = (NF + SL - 1) / SL;
+#pragma unroll
+    for (int rb = 0; rb < R; ++rb)
+#pragma unroll
+      for (int cb = 0; cb < CM; ++cb) {
+        const int i = rb * CM + cb;
+        if constexpr (NRB > 0) {
+#pragma unroll
+          for (int f = 0; f < RPS; ++f)
+            if (i * RPS + f < NF) read_frag(rs, rks, (ks & 1) ^ 1, i * RPS + f);
+          acc[rb][cb] = mma<T>(fb[ks & 1][cb], fa[ks & 1][rb], acc[rb][cb]);
+        }
+#pragma unroll
+        for (int l = 0; l < PER; ++l)
+          if ((2 * l + 1) * SL / (2 * PER) == (NRB > 0 ? i : 0) && (NRB > 0 || cb == 0) && slot * PER + l < LPS)
+            issue(fill, fstage, slot * PER + l);
+      }
   };
 
   if (nk > 0) {
@@ -531,15 +571,22 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
   for (; kb + ST < nk; ++kb) {
     const int nxt = cur + 1 == ST ? 0 : cur + 1;
     wait_barrier<LPS*(ST - 2)>();
-    read_frags(nxt, 0, 0);
-    prepare(kb + ST);
-    hold_order();
-    multiply(KS - 1, std::true_type{}, 0, kb + ST, cur);
+    if constexpr (MT == 16) {
+      prepare(kb + ST);
+      interleaved(KS - 1, nxt, 0, 0, kb + ST, cur);
 #pragma unroll
-    for (int ks = 0; ks + 1 < KS; ++ks) {
-      read_frags(nxt, ks + 1, (ks + 1) & 1);
+      for (int ks = 0; ks + 1 < KS; ++ks) interleaved(ks, nxt, ks + 1, ks + 1, kb + ST, cur);
+    } else {
+      read_frags(nxt, 0, 0);
+      prepare(kb + ST);
       hold_order();
-      multiply(ks, std::true_type{}, ks + 1, kb + ST, cur);
+      multiply(KS - 1, std::true_type{}, 0, kb + ST, cur);
+#pragma unroll
+      for (int ks = 0; ks + 1 < KS; ++ks) {
+        read_frags(nxt, ks + 1, (ks + 1) & 1);
+        hold_order();
+        multiply(ks, std::true_type{}, ks + 1, kb + ST, cur);
+      }
     }
     cur = nxt;
   }
@@ -567,49 +614,46 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
     cur = nxt;
   }
 
-  // Accumulator element i of lane (half, l32): row l32 of the row block, column
-  // 8 (i / 4) + 4 half + i % 4 of the column block. Each wave passes a row block through its
-  // part of the stages, so that it stores whole runs of a row (128 bytes of 16-bit outputs)
+  // Accumulator element i of lane (part, lm): row lm of the row block, column
+  // 8 (i / 4) + 4 part + i % 4 of the column block. Each wave passes a row block through
+  // its part of the stages, so that it stores whole runs of a row (128 bytes of 16-bit outputs)
   // instead of 8 bytes per row.
   lds_barrier();
   if constexpr (NRB > 0) {
     char* mine = lds + wave * (ST * F::STAGE / (WM * WN));
     const int col0 = c0 + wn * CB * 32;
-    float bs[CB][4][4];
+    float bs[CM][AV];
     if constexpr (T == kI8) {
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
+      for (int cb = 0; cb < CM; ++cb)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int col = col0 + cb * 32 + 8 * q + 4 * half + j;
-            bs[cb][q][j] = g.b_scale[(size_t)e * g.N + (col < g.N ? col : g.N - 1)];
-          }
+        for (int i = 0; i < AV; ++i) {
+          const int col = col0 + cb * MT + 8 * (i >> 2) + 4 * part + (i & 3);
+          bs[cb][i] = g.b_scale[(size_t)e * g.N + (col < g.N ? col : g.N - 1)];
+        }
     }
     const size_t out0 = OP == kDw ? (size_t)e * g.N + m0 : (size_t)base;
     auto value = [&](int rb, int cb, int i, float rs) -> float {
       float v = (float)acc[rb][cb][i];
       if constexpr (T == kI8) {
-        v = v * rs * bs[cb][i >> 2][i & 3];
+        v = v * rs * bs[cb][i];
         // the output is this fp32 value rounded again: kept apart from the narrowing, which the
         // backend would fold into one mixed-precision multiply
         asm volatile("" : "+v"(v));
       }
       return v;
     };
+    auto scale = [&](int rb) { return T == kI8 ? g.a_scale[s_src[wm * RB * 32 + rb * MT + lm]] : 1.f; };
     if (g.out_dtype == 0)
-      store_rows<4, CB, NRB, OP != kFwd || T != kI8>(
-          g, mine, value, [&](int rb) { return T == kI8 ? g.a_scale[s_src[(wm * RB + rb) * 32 + l32]] : 1.f; }, wm * RB * 32, mlim, out0, col0, nout);
+      store_rows<4, MT, CB, NRB, OP != kFwd || T != kI8>(g, mine, value, scale, wm * RB * 32, mlim, out0, col0, nout);
     else
-      store_rows<2, CB, NRB, OP != kFwd || T != kI8>(
-          g, mine, value, [&](int rb) { return T == kI8 ? g.a_scale[s_src[(wm * RB + rb) * 32 + l32]] : 1.f; }, wm * RB * 32, mlim, out0, col0, nout);
+      store_rows<2, MT, CB, NRB, OP != kFwd || T != kI8>(g, mine, value, scale, wm * RB * 32, mlim, out0, col0, nout);
   }
 }
 
-template <int OP, int T, int WM, int WN, int RB, int CB, int JB, int ST>
+template <int OP, int T, int WM, int WN, int RB, int CB, int MT, int JB, int ST>
 __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, int NB) {
-  typedef Cfg<OP, T, WM, WN, RB, CB, JB, ST> F;
+  typedef Cfg<OP, T, WM, WN, RB, CB, MT, JB, ST> F;
   __shared__ __attribute__((aligned(256))) char lds[ST * F::STAGE];
   __shared__ int s_src[OP == kDw ? kIdxTile : F::BM];
   if constexpr (OP == kDw) {
@@ -622,7 +666,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, 
     const int mb = tile / NB, nb = tile - mb * NB;
     const int lo = uni(clampi(g.offsets[e], 0, g.P)), hi = uni(clampi(g.offsets[e + 1], lo, g.P));
     // an expert without rows has a zero gradient: no K-block, the cleared accumulator is stored
-    tile_product<OP, T, WM, WN, RB, CB, JB, ST, RB>(g, e, lo, 0, mb * F::BM, nb * F::BN, hi - lo, lds, s_src);
+    tile_product<OP, T, WM, WN, RB, CB, MT, JB, ST, RB>(g, e, lo, 0, mb * F::BM, nb * F::BN, hi - lo, lds, s_src);
   } else {
     Tile t;
     if (!find_tile<F::THREADS>(g, F::BM, NB, t)) return;
@@ -635,7 +679,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, 
     const int c0 = t.nb * F::BN, C = OP == kFwd ? g.K : g.N;
     // occupied row blocks of this wave's row of waves (the same in all its lanes)
     const int nrb = uni(clampi(((t.rows + 31) >> 5) - (int)(threadIdx.x >> 6) / WN * RB, 0, RB));
-#define NVFP4_TILE(NRB) tile_product<OP, T, WM, WN, RB, CB, JB, ST, NRB>(g, t.e, base, t.rows, 0, c0, C, lds, s_src)
+#define NVFP4_TILE(NRB) tile_product<OP, T, WM, WN, RB, CB, MT, JB, ST, NRB>(g, t.e, base, t.rows, 0, c0, C, lds, s_src)
     if (nrb == RB)
       NVFP4_TILE(RB);
     else if (RB > 3 && nrb == 3)
@@ -742,7 +786,7 @@ __global__ __launch_bounds__(256) void stream_kernel(GroupedArgs g, int NB) {
 #pragma unroll
       for (int q = 0; q < NW; ++q)
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) acc[q][rb] = mma16<T>(w[q][u], x[rb][u], acc[q][rb]);
+        for (int rb = 0; rb < RB; ++rb) acc[q][rb] = mma<T>(w[q][u], x[rb][u], acc[q][rb]);
   }
 #pragma unroll
   for (int q = 0; q < NW; ++q)
@@ -785,9 +829,9 @@ static unsigned grid_rows(const GroupedArgs& g, int bm, int NB) {
   return (unsigned)((tiles * NB + 7) / 8 * 8);
 }
 
-template <int OP, int T, int WM, int WN, int RB, int CB, int JB, int ST>
+template <int OP, int T, int WM, int WN, int RB, int CB, int MT, int JB, int ST>
 static hipError_t launch_cfg(const GroupedArgs& g, hipStream_t st) {
-  typedef Cfg<OP, T, WM, WN, RB, CB, JB, ST> F;
+  typedef Cfg<OP, T, WM, WN, RB, CB, MT, JB, ST> F;
   const int nout = OP == kFwd ? g.N : g.K;
   const int NB = (nout + F::BN - 1) / F::BN;
   unsigned grid;
@@ -795,7 +839,7 @@ static hipError_t launch_cfg(const GroupedArgs& g, hipStream_t st) {
     grid = (unsigned)((long long)g.E * (((g.N + F::BM - 1) / F::BM * NB + 7) / 8) * 8);
   else
     grid = grid_rows(g, F::BM, NB);
-  grouped_kernel<OP, T, WM, WN, RB, CB, JB, ST><<<grid, F::THREADS, 0, st>>>(g, NB);
+  grouped_kernel<OP, T, WM, WN, RB, CB, MT, JB, ST><<<grid, F::THREADS, 0, st>>>(g, NB);
   return hipGetLastError();
 }
 
@@ -820,14 +864,15 @@ struct Load {
 static int64_t blocks(int64_t n, int b) { return (n + b - 1) / b; }
 
 // The largest tile that still fills the device, because a larger tile reads less per product:
-//   256 x 256, 8 waves, one block per CU, four 64-byte stages
+//   256 x 256, 8 waves, one block per CU: forward two 128-byte stages and 16 x 16 matrix
+//     instructions, the gradients four 64-byte stages and 32 x 32
 //   128 x 256, 4 waves, two blocks per CU, three stages: less of a tile is empty at the end
 //     of an expert, and one block's stores overlap the other's products
 //   64 x 128, 4 waves, two blocks per CU, three 128-byte stages
 //   64 x 64, 4 waves, four 128-byte stages
 // Measured, us (top 8, 2048 -> 1536 in bf16 unless said): 64 experts, 8192 tokens, forward
-// 256 x 256 437, 128 x 256 472, 64 x 128 600; dx 440 / 435 / 670; 8 experts, forward 117 /
-// 132 / 155; 512 experts, uniform, 32 rows each: 128 x 256 595, 64 x 128 588; 64 rows each
+// 256 x 256 406 (as the gradients 419), 128 x 256 472, 64 x 128 600; dx 440 (as the forward
+// 475) / 435 / 670; dense int8 8192 x 4096 x 4096 117 (133); 8 experts, forward 113 / 132 / 155; 512 experts, uniform, 32 rows each: 128 x 256 595, 64 x 128 588; 64 rows each
 // 648 / 714; dx of 8 rows each 459 / 479. Dense int8 2048 x 4096 x 4096 (256 tiles of
 // 128 x 256): 45, 64 x 128 72; 1024 rows (128 tiles): 38 / 36, 64 x 64 42; 512 rows 34 / 24 /
 // 23; 128 rows 33 / 15 / 11.
@@ -836,10 +881,10 @@ static hipError_t launch_tiles(const GroupedArgs& g, const Load& l, hipStream_t 
   const int nout = OP == kFwd ? g.N : g.K;
   const int64_t t128 = l.tiles(128) * blocks(nout, 256);
   if (l.rows >= (OP == kFwd ? 512 : 1024) && l.tiles(256) * blocks(nout, 256) >= 256)
-    return launch_cfg<OP, T, 2, 4, 4, 2, 64, 4>(g, st);
-  if (t128 >= 192 && (OP == kDx || l.rows >= 48)) return launch_cfg<OP, T, 1, 4, 4, 2, 64, 3>(g, st);
-  if (l.tiles(64) * blocks(nout, 128) >= 300) return launch_cfg<OP, T, 1, 4, 2, 1, 128, 3>(g, st);
-  return launch_cfg<OP, T, 2, 2, 1, 1, 128, 4>(g, st);
+    return launch_cfg<OP, T, 2, 4, 4, 2, OP == kFwd ? 16 : 32, OP == kFwd ? 128 : 64, OP == kFwd ? 2 : 4>(g, st);
+  if (t128 >= 192 && (OP == kDx || l.rows >= 48)) return launch_cfg<OP, T, 1, 4, 4, 2, 32, 64, 3>(g, st);
+  if (l.tiles(64) * blocks(nout, 128) >= 300) return launch_cfg<OP, T, 1, 4, 2, 1, 32, 128, 3>(g, st);
+  return launch_cfg<OP, T, 2, 2, 1, 1, 32, 128, 4>(g, st);
 }
 
 template <int T>
@@ -874,8 +919,8 @@ template <int T>
 static hipError_t weight_gradient(const GroupedArgs& g, hipStream_t st) {
   // 256 x 256 while that fills the device: 64 experts of 1536 x 2048, 8192 tokens 472 us, 128 x 128
   // 526; 13 experts of 520 x 392 (78 tiles) 20.0, 128 x 128 12.5
-  if (g.E * blocks(g.N, 256) * blocks(g.K, 256) >= 256) return launch_cfg<kDw, T, 2, 4, 4, 2, 64, 4>(g, st);
-  return launch_cfg<kDw, T, 2, 2, 2, 2, 64, 3>(g, st);
+  if (g.E * blocks(g.N, 256) * blocks(g.K, 256) >= 256) return launch_cfg<kDw, T, 2, 4, 4, 2, 32, 64, 4>(g, st);
+  return launch_cfg<kDw, T, 2, 2, 2, 2, 32, 64, 3>(g, st);
 }
 
 hipError_t launch_grouped_dw(int type, const GroupedArgs& g, hipStream_t st) {
