@@ -152,6 +152,63 @@ def test_grouped_exact_on_small_integers(case, t, gather):
     assert bool((out[r.used:] == SENTINEL).all()) and bool((dx[r.used:] == SENTINEL).all()), "rows behind the last"
 
 
+# Loads that reach every tile of the forward product and of the gradients, with partial row
+# tiles, column tiles and K-blocks in each: (rows per expert, topk, N, K)
+LOADS = {
+    "stream two groups": ([1, 2, 0, 1] * 15, 1, 520, 264),
+    "stream 32 rows": ([20, 0, 31, 33, 100], 1, 136, 264),
+    "64 x 64": ([200, 0, 65, 250, 1], 2, 264, 2056),
+    "64 x 128": ([40, 1, 0, 33, 65, 2, 64, 7] * 5, 2, 1032, 136),
+    "128 x 256": ([300, 60, 130, 1, 0, 515], 2, 5128, 328),
+    "256 x 256": ([700, 2101], 1, 5640, 200),
+    "256 x 256, one K-block": ([513, 1500], 1, 8200, 48),
+    "gradients of few rows": ([1, 0, 3] * 80, 1, 264, 520),
+    "gradients of many rows": ([1029, 2300, 31], 1, 520, 5640),
+    "weights of many experts": ([1, 0, 70] * 90 + [2113], 1, 136, 72),
+}
+
+
+@pytest.mark.parametrize("load", LOADS.values(), ids=LOADS.keys())
+def test_every_tile_exact(load):
+    r, (N, K) = routing_of(load), load[2:]
+    src = r.src(True)
+    for t in (BF16, F16):
+        x, w, dy = draw((r.T, K), t, 2, ints=True), draw((r.E, N, K), t, 3, ints=True), draw((r.rows, N), t, 4, ints=True)
+        xd, wd, dyd = x.to(DEV), w.to(DEV), dy.to(DEV)
+        out = torch.full((r.rows, N), SENTINEL, device=DEV)
+        nv.grouped_linear(xd, wd, r.off, r.pairs, r.topk, out=out)
+        dx = torch.full((r.rows, K), SENTINEL, device=DEV)
+        nv.grouped_linear_dx(dyd, wd, r.off, out=dx)
+        dw = nv.grouped_linear_dw(dyd, xd, r.off, r.pairs, r.topk, out_dtype=F32)
+        # sums of integers below 2^24: float32 products on the CPU are exact too
+        for e, a, b in r.spans():
+            xe, de = x[src[a:b]].float(), dy[a:b].float()
+            assert torch.equal(out[a:b].cpu(), xe @ w[e].float().t()), ("forward", e)
+            assert torch.equal(dx[a:b].cpu(), de @ w[e].float()), ("dx", e)
+            assert torch.equal(dw[e].cpu(), de.t() @ xe), ("dw", e)
+        assert bool((out[r.used:] == SENTINEL).all()) and bool((dx[r.used:] == SENTINEL).all())
+    K = -(-K // 16) * 16
+    q, sx = quantized(r.T, K, 3)
+    w8, sw = quantized(r.E * (N + 1), K, 4)
+    w8, sw = w8.reshape(r.E, N + 1, K), sw.reshape(r.E, N + 1)
+    for od in (F32, F16):
+        y = nv.grouped_linear_i8(q.to(DEV), sx.to(DEV), w8.to(DEV), sw.to(DEV), r.off, r.pairs, r.topk, out_dtype=od)
+        for e, a, b in r.spans():
+            acc = (q[src[a:b]].double() @ w8[e].double().t()).to(torch.int32)
+            assert torch.equal(y[a:b].cpu(), scaled(acc, sx[src[a:b]], sw[e], od)), (e, od)
+
+
+@pytest.mark.parametrize("T,N,K", [(2049, 4100, 144), (700, 9001, 528), (8200, 2048, 64)])
+def test_linear_i8_of_many_rows(T, N, K):
+    """The larger tiles with one expert (no offsets)."""
+    x, sx = quantized(T, K, 1)
+    w, sw = quantized(N, K, 2)
+    for od in (BF16, F32):
+        y = nv.linear_i8(x.to(DEV), sx.to(DEV), w.to(DEV), sw.to(DEV), out_dtype=od)
+        # sums up to 528 * 2^14 < 2^24: exact in fp32
+        assert torch.equal(y.cpu(), scaled((x.float() @ w.float().t()).to(torch.int32), sx, sw, od))
+
+
 @pytest.mark.parametrize("od", [F32, BF16, F16])
 @pytest.mark.parametrize("t", [BF16, F16])
 @pytest.mark.parametrize("case", [CASES[i] for i in (2, 3, 5)], ids=[IDS[i] for i in (2, 3, 5)])
