@@ -464,8 +464,8 @@ int nvfp4_grouped_linear_dw(const void* dy, const void* x, int32_t x_rows, int32
  * order, of topk_weights[t][j] * y[pos][h], pos the row with sorted_pairs[pos] == t * topk +
  * j; a dropped pair (in no row) adds nothing. topk_weights float [T][topk], or NULL for
  * weights of 1. y [T*topk][H] in y_dtype, out [T][H] in out_dtype (fp32 sum, rounded once).
- * ws needs nvfp4_moe_combine_workspace_size() bytes, any contents; calls sharing one must
- * not overlap. T == 0 is a no-op. A pair listed twice (which nvfp4_moe_route never does)
+ * ws needs nvfp4_moe_combine_workspace_size() bytes, any contents (0 up to 1024 pairs: ws may
+ * then be NULL); calls sharing one must not overlap. T == 0 is a no-op. A pair listed twice (which nvfp4_moe_route never does)
  * counts once.
  * Errors: EINVAL for null or misaligned pointers (y, out, ws 16-byte aligned), T < 0,
  * topk < 1, H < 1, unknown dtypes; EUNSUPPORTED for T * topk above 2^30, H above 2^20 or

@@ -571,10 +571,10 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _same_device(dev: torch.device, **tensors: Optional[torch.Tensor]) -> None:
-    for name, t in tensors.items():
+def _same_device(dev: torch.device, *tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
         if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+            raise ValueError(f"a tensor of {tuple(t.shape)} is on {t.device}, expected {dev}")
 
 
 def _call(fn: str, dev: torch.device, *args) -> None:
@@ -582,9 +582,9 @@ def _call(fn: str, dev: torch.device, *args) -> None:
     if dev.type != "cuda":
         raise ValueError(f"the library's device calls take GPU tensors (got {dev})")
     f = getattr(_lib or load_library(), fn)
-    # the raw handle: torch.cuda.current_stream() builds an object, a fifth of a small call's time
+    # the raw handles: torch.cuda.current_stream() builds an object, a fifth of a small call's time
     stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         status = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -598,7 +598,7 @@ def _out(out: Optional[torch.Tensor], shape, dtype: torch.dtype, dev: torch.devi
         return torch.empty(shape, dtype=dtype, device=dev)
     if tuple(out.shape) != tuple(shape) or out.dtype not in DTYPE:
         raise ValueError(f"out must be a {tuple(shape)} library-dtype tensor")
-    _same_device(dev, out=out)
+    _same_device(dev, out)
     return out
 
 
@@ -613,7 +613,7 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     _need(x_scale.dtype == torch.float32 and x_scale.numel() == T and w_scale.dtype == torch.float32
           and w_scale.numel() == N, "x_scale and w_scale must be float32 [T] and [N]")
     dev = x.device
-    _same_device(dev, x_scale=x_scale, w=w, w_scale=w_scale)
+    _same_device(dev, x_scale, w, w_scale)
     out = _out(out, (T, N), out_dtype, dev)
     _call("nvfp4_linear_i8", dev, _ptr(x), _ptr(x_scale), T, _ptr(w), _ptr(w_scale), N, K, _ptr(out),
           DTYPE[out.dtype])
@@ -624,12 +624,12 @@ def _grouped_rows(x_rows: int, offsets: torch.Tensor, E: int, pairs: Optional[to
                   dev: torch.device) -> int:
     """Checks the routing of a grouped call; returns its number of sorted rows."""
     _need(offsets.dtype == torch.int32 and offsets.numel() == E + 1, "expert_offsets must be int32 [E+1]")
-    _same_device(dev, expert_offsets=offsets)
+    _same_device(dev, offsets)
     if pairs is None:
         return x_rows
     _need(pairs.dtype == torch.int32 and pairs.dim() == 1 and topk >= 1 and pairs.numel() == x_rows * topk,
           "sorted_pairs must be int32 [x_rows * topk]")
-    _same_device(dev, sorted_pairs=pairs)
+    _same_device(dev, pairs)
     return x_rows * topk
 
 
@@ -647,7 +647,7 @@ def grouped_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w
     _need(x_scale.dtype == torch.float32 and x_scale.numel() == T and w_scale.dtype == torch.float32
           and tuple(w_scale.shape) == (E, N), "x_scale and w_scale must be float32 [T] and [E][N]")
     dev = x.device
-    _same_device(dev, x_scale=x_scale, w=w, w_scale=w_scale)
+    _same_device(dev, x_scale, w, w_scale)
     rows = _grouped_rows(T, expert_offsets, E, sorted_pairs, topk, dev)
     out = _out(out, (rows, N), out_dtype, dev)
     _call("nvfp4_grouped_linear_i8", dev, _ptr(x), _ptr(x_scale), T, _ptr(w), _ptr(w_scale), _ptr(expert_offsets), E,
@@ -667,7 +667,7 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tenso
     T, K = x.shape
     E, N = w.shape[0], w.shape[1]
     dev = x.device
-    _same_device(dev, w=w)
+    _same_device(dev, w)
     rows = _grouped_rows(T, expert_offsets, E, sorted_pairs, topk, dev)
     out = _out(out, (rows, N), out_dtype or x.dtype, dev)
     _call("nvfp4_grouped_linear", dev, _ptr(x), T, _ptr(w), DTYPE[x.dtype], _ptr(expert_offsets), E,
@@ -684,7 +684,7 @@ def grouped_linear_dx(dy: torch.Tensor, w: torch.Tensor, expert_offsets: torch.T
     rows, N = dy.shape
     E, K = w.shape[0], w.shape[2]
     dev = dy.device
-    _same_device(dev, w=w)
+    _same_device(dev, w)
     _grouped_rows(rows, expert_offsets, E, None, 1, dev)
     out = _out(out, (rows, K), out_dtype or dy.dtype, dev)
     _call("nvfp4_grouped_linear_dx", dev, _ptr(dy), _ptr(w), DTYPE[dy.dtype], _ptr(expert_offsets), E, rows, N, K,
@@ -702,7 +702,7 @@ def grouped_linear_dw(dy: torch.Tensor, x: torch.Tensor, expert_offsets: torch.T
     T, K = x.shape
     E, N = expert_offsets.numel() - 1, dy.shape[1]
     dev = dy.device
-    _same_device(dev, x=x)
+    _same_device(dev, x)
     rows = _grouped_rows(T, expert_offsets, E, sorted_pairs, topk, dev)
     _need(dy.shape[0] == rows, "dy must have one row per sorted row")
     out = _out(out, (E, N, K), out_dtype or dy.dtype, dev)
@@ -715,13 +715,16 @@ def combine_workspace_size(T: int, topk: int) -> int:
     return int(load_library().nvfp4_moe_combine_workspace_size(T, topk))
 
 
-def _combine_ws(ws: Optional[torch.Tensor], T: int, topk: int, dev: torch.device) -> torch.Tensor:
-    need = combine_workspace_size(T, topk)
+def _combine_ws(ws: Optional[torch.Tensor], T: int, topk: int, dev: torch.device):
+    """(tensor or None, pointer, bytes) of the workspace; a new one's contents do not matter."""
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
+        need = combine_workspace_size(T, topk)
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _need(ws.dtype == torch.uint8, "ws must be uint8")
-    _same_device(dev, ws=ws)
-    return ws
+    _same_device(dev, ws)
+    return ws, _ptr(ws), ws.numel()
 
 
 def moe_combine(y: torch.Tensor, sorted_pairs: torch.Tensor, topk: int, w: Optional[torch.Tensor] = None,
@@ -735,11 +738,11 @@ def moe_combine(y: torch.Tensor, sorted_pairs: torch.Tensor, topk: int, w: Optio
     T, H = y.shape[0] // topk, y.shape[1]
     _need(w is None or (w.dtype == torch.float32 and w.numel() == T * topk), "w must be float32 [T][topk]")
     dev = y.device
-    _same_device(dev, sorted_pairs=sorted_pairs, w=w)
+    _same_device(dev, sorted_pairs, w)
     out = _out(out, (T, H), out_dtype or y.dtype, dev)
-    ws = _combine_ws(ws, T, topk, dev)
+    ws, ws_ptr, ws_bytes = _combine_ws(ws, T, topk, dev)
     _call("nvfp4_moe_combine", dev, _ptr(y), DTYPE[y.dtype], _ptr(sorted_pairs), _ptr(w), T, topk, H, _ptr(out),
-          DTYPE[out.dtype], _ptr(ws), ws.numel())
+          DTYPE[out.dtype], ws_ptr, ws_bytes)
     return out
 
 
@@ -755,11 +758,11 @@ def moe_combine_grad(dout: torch.Tensor, y: torch.Tensor, sorted_pairs: torch.Te
     T, H = dout.shape
     topk = w.shape[1]
     dev = y.device
-    _same_device(dev, dout=dout, sorted_pairs=sorted_pairs, w=w)
+    _same_device(dev, dout, sorted_pairs, w)
     dy = _out(dy, tuple(y.shape), y.dtype, dev)
     _need(dy.dtype == y.dtype, "dy must have y's dtype")
     dw = torch.empty_like(w)
-    ws = _combine_ws(ws, T, topk, dev)
+    ws, ws_ptr, ws_bytes = _combine_ws(ws, T, topk, dev)
     _call("nvfp4_moe_combine_grad", dev, _ptr(dout), _ptr(y), DTYPE[y.dtype], _ptr(sorted_pairs), _ptr(w), T, topk, H,
-          _ptr(dy), _ptr(dw), _ptr(ws), ws.numel())
+          _ptr(dy), _ptr(dw), ws_ptr, ws_bytes)
     return dy, dw

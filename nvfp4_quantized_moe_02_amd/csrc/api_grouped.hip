@@ -120,15 +120,17 @@ int nvfp4_grouped_linear_dw(const void* dy, const void* x, int32_t x_rows, int32
 
 size_t nvfp4_moe_combine_workspace_size(int32_t T, int32_t topk) {
   if (T < 0 || topk < 1) return 0;
-  return ((size_t)T * topk * 4 + 255) / 256 * 256 + 256;
+  const int64_t P = (int64_t)T * topk;
+  return P <= kSmallPairs ? 0 : ((size_t)P * 4 + 255) / 256 * 256;
 }
 
 static int check_combine(const int32_t* pairs, const float* w, int32_t T, int32_t topk, int32_t H, const void* ws,
                          size_t ws_bytes) {
-  if (T < 0 || topk < 1 || H < 1 || !ws || (T > 0 && !pairs)) return NVFP4_EINVAL;
+  const size_t need = nvfp4_moe_combine_workspace_size(T, topk);
+  if (T < 0 || topk < 1 || H < 1 || (need > 0 && !ws) || (T > 0 && !pairs)) return NVFP4_EINVAL;
   if (!aligned(pairs, 4) || !aligned(w, 4) || !aligned(ws, 16)) return NVFP4_EINVAL;
   if ((int64_t)T * topk > kMaxRows || H > kMaxWidth || (int64_t)T * H >= (int64_t)1 << 38) return NVFP4_EUNSUPPORTED;
-  if (ws_bytes < nvfp4_moe_combine_workspace_size(T, topk)) return NVFP4_EWORKSPACE;
+  if (ws_bytes < need) return NVFP4_EWORKSPACE;
   return NVFP4_OK;
 }
 

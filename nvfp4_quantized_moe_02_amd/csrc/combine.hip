@@ -19,7 +19,6 @@ namespace nvfp4 {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kSmallPairs = 1024;
 constexpr int kSlots = 8;  // rows of a token in flight together
 
 __global__ __launch_bounds__(256) void invert_kernel(const int32_t* __restrict__ pairs, int P,

@@ -26,7 +26,8 @@ hipError_t launch_grouped_fwd(int type, const GroupedArgs& g, hipStream_t st);
 hipError_t launch_grouped_dx(int type, const GroupedArgs& g, hipStream_t st);
 hipError_t launch_grouped_dw(int type, const GroupedArgs& g, hipStream_t st);
 
-// combine.hip. inv: workspace of P = T * topk ints (any contents).
+// combine.hip. inv: workspace of P = T * topk ints (any contents); none up to kSmallPairs.
+constexpr int kSmallPairs = 1024;
 struct CombineArgs {
   const int32_t* pairs;  // sorted pairs [P], -1 for dropped ones
   const float* w;        // [T][topk] or nullptr (1)

@@ -412,7 +412,7 @@ def test_combine(T, topk, H, drop, t):
     # the gradients, on a workspace of any contents
     dy = torch.full((P, H), SENTINEL, dtype=t, device=DEV)
     for fill in (0, 255):
-        ws = torch.full((nv.combine_workspace_size(T, topk),), fill, dtype=torch.uint8, device=DEV)
+        ws = torch.full((max(nv.combine_workspace_size(T, topk), 16),), fill, dtype=torch.uint8, device=DEV)
         _, dw = nv.moe_combine_grad(dd, yd, r.pairs, wd, dy=dy, ws=ws)
         d = dout[tok].double()
         # one fp32 product, then one rounding to the type
@@ -436,7 +436,7 @@ def test_another_stream_and_a_replayed_graph():
     r = Routing([3, 0, 150, 40], 97, 2)
     x, w = draw((r.T, 72), BF16, 1).to(DEV), draw((4, 264, 72), BF16, 2).to(DEV)
     wts = torch.rand(r.T, 2, device=DEV)
-    ws = torch.empty(nv.combine_workspace_size(r.T, 2), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(max(nv.combine_workspace_size(r.T, 2), 16), dtype=torch.uint8, device=DEV)
     y, out = torch.zeros((r.rows, 264), dtype=BF16, device=DEV), torch.zeros((r.T, 264), dtype=BF16, device=DEV)
     dw = torch.zeros((4, 264, 72), dtype=BF16, device=DEV)
 

@@ -85,9 +85,9 @@ def combine_grad(dout=P, y=P, yd=BF16, pairs=P, w=P, T=4, topk=2, H=64, out=P, d
 
 @pytest.mark.parametrize("fn", [combine, combine_grad])
 @pytest.mark.parametrize("kw,want", [
-    (dict(y=None), EINVAL), (dict(pairs=None), EINVAL), (dict(out=None), EINVAL), (dict(ws=None), EINVAL),
+    (dict(y=None), EINVAL), (dict(pairs=None), EINVAL), (dict(out=None), EINVAL), (dict(ws=None, T=1024), EINVAL),
     (dict(T=-1), EINVAL), (dict(topk=0), EINVAL), (dict(H=0), EINVAL), (dict(yd=3), EINVAL), (dict(y=P + 2), EINVAL),
-    (dict(out=P + 2), EINVAL), (dict(ws=P + 4), EINVAL), (dict(w=P + 2), EINVAL), (dict(wsb=255), EWS),
+    (dict(out=P + 2), EINVAL), (dict(ws=P + 4), EINVAL), (dict(w=P + 2), EINVAL), (dict(wsb=8191, T=1024), EWS),
     (dict(T=1 << 30, topk=2), EUNSUP), (dict(H=(1 << 20) + 1), EUNSUP), (dict(T=0, y=None, pairs=None, out=None), OK),
 ])
 def test_combine_refusals(fn, kw, want):
@@ -97,6 +97,8 @@ def test_combine_refusals(fn, kw, want):
 def test_combine_workspace():
     lib = B.load_library()
     assert lib.nvfp4_moe_combine_workspace_size(8192, 8) >= 8192 * 8 * 4
+    assert lib.nvfp4_moe_combine_workspace_size(128, 8) == 0  # small lists need none
+    assert lib.nvfp4_moe_combine_workspace_size(129, 8) >= 129 * 8 * 4
     assert lib.nvfp4_moe_combine_workspace_size(-1, 8) == 0
     assert lib.nvfp4_moe_combine_workspace_size(1, 0) == 0
     assert combine_grad(dout=None) == EINVAL
