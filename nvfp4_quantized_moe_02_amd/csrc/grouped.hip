@@ -155,6 +155,45 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int bm, int NB, 
   return t.rows > 0;  // 0: offsets that do not ascend, whose counts disagree
 }
 
+// The slot-th expert of the order in which those with at least the average number of rows come
+// first (each half in expert order). A gradient tile takes as long as its expert has rows, so
+// the long ones must not come last.
+template <int THREADS>
+__device__ __forceinline__ int busy_first(const GroupedArgs& g, int slot) {
+  __shared__ int s_tot[THREADS / 64];
+  __shared__ int s_e;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per_t = (g.E + THREADS - 1) / THREADS;
+  const int e0 = tid * per_t < g.E ? tid * per_t : g.E, e1 = e0 + per_t < g.E ? e0 + per_t : g.E;
+  auto busy = [&](int e) {
+    const int lo = clampi(g.offsets[e], 0, g.P);
+    return (long long)(clampi(g.offsets[e + 1], lo, g.P) - lo) * g.E >= g.P;
+  };
+  int cnt = 0;
+  for (int e = e0; e < e1; ++e) cnt += busy(e);
+  int inc = cnt;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 63) s_tot[wave] = inc;
+  __syncthreads();
+  int before = inc - cnt, all = 0;  // busy experts before e0, and in all
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    if (w < wave) before += s_tot[w];
+    all += s_tot[w];
+  }
+  for (int e = e0; e < e1; ++e) {
+    const bool b = busy(e);
+    if ((b ? before : all + e - before) == slot) s_e = e;
+    before += b;
+  }
+  __syncthreads();
+  return uni(s_e);
+}
+
 template <int T>
 struct Acc {
   typedef f32x16_t v32;
@@ -652,7 +691,7 @@ __device__ __forceinline__ void tile_product(const GroupedArgs& g, int e, int ba
 }
 
 template <int OP, int T, int WM, int WN, int RB, int CB, int MT, int JB, int ST>
-__global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, int NB) {
+__global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, int NB, bool ordered) {
   typedef Cfg<OP, T, WM, WN, RB, CB, MT, JB, ST> F;
   __shared__ __attribute__((aligned(256))) char lds[ST * F::STAGE];
   __shared__ int s_src[OP == kDw ? kIdxTile : F::BM];
@@ -661,8 +700,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_kernel(GroupedArgs g, 
     // with many rows do not gather on one; which eighth turns with the expert.
     const int tiles = (g.N + F::BM - 1) / F::BM * NB, per = (tiles + 7) >> 3;
     const int j = blockIdx.x >> 3;
-    const int e = j / per, tile = ((blockIdx.x + e) & 7) * per + (j - e * per);
+    const int slot = j / per, tile = ((blockIdx.x + slot) & 7) * per + (j - slot * per);
     if (tile >= tiles) return;
+    const int e = ordered ? busy_first<F::THREADS>(g, slot) : slot;
     const int mb = tile / NB, nb = tile - mb * NB;
     const int lo = uni(clampi(g.offsets[e], 0, g.P)), hi = uni(clampi(g.offsets[e + 1], lo, g.P));
     // an expert without rows has a zero gradient: no K-block, the cleared accumulator is stored
@@ -834,12 +874,15 @@ static hipError_t launch_cfg(const GroupedArgs& g, hipStream_t st) {
   typedef Cfg<OP, T, WM, WN, RB, CB, MT, JB, ST> F;
   const int nout = OP == kFwd ? g.N : g.K;
   const int NB = (nout + F::BN - 1) / F::BN;
+  // dw: the search costs a block about a microsecond. 64 experts of 1024 rows on average under Zipf
+  // routing 470 -> 448 us, 8 of 2048 131 -> 118; 64 of 128 rows 156 -> 162, 512 of 32 807 -> 830.
+  const bool ordered = OP == kDw && g.E > 1 && g.P / g.E >= 256;
   unsigned grid;
   if (OP == kDw)
     grid = (unsigned)((long long)g.E * (((g.N + F::BM - 1) / F::BM * NB + 7) / 8) * 8);
   else
     grid = grid_rows(g, F::BM, NB);
-  grouped_kernel<OP, T, WM, WN, RB, CB, MT, JB, ST><<<grid, F::THREADS, 0, st>>>(g, NB);
+  grouped_kernel<OP, T, WM, WN, RB, CB, MT, JB, ST><<<grid, F::THREADS, 0, st>>>(g, NB, ordered);
   return hipGetLastError();
 }
 
