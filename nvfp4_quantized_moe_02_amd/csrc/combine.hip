@@ -10,9 +10,11 @@
 //
 // A wave works on one token, so its positions are scalars and its row loads are issued
 // together without lane-dependent branches. Measured, 8192 tokens of 8 slots, 2048 columns of
-// bf16: forward 60 us, gradient 95 us (5.0 and 6.0 TB/s of what has to move); with one thread
-// per 8 columns of a token, each looking up its own positions, 104 and 196 us; without the
-// non-temporal loads 66 and 114 us; with non-temporal stores too 57 and 115 us.
+// bf16: forward 60 us, gradient 115 us (5.0 TB/s of what has to move in both; the gradient 94
+// when its output buffer stays in the cache from the call before); with one thread per 8
+// columns of a token, each looking up its own positions, 104 and 194 us; without the
+// non-temporal loads 68 and 124 us. Non-temporal stores gain the forward 3 us, but then its
+// output, which the next operator reads, is not in the cache.
 #include "grouped.h"
 
 namespace nvfp4 {

@@ -966,9 +966,13 @@ hipError_t launch_grouped_dx(int type, const GroupedArgs& g, hipStream_t st) {
 template <int T>
 static hipError_t weight_gradient(const GroupedArgs& g, hipStream_t st) {
   // 256 x 256 while that fills the device: 64 experts of 1536 x 2048, 8192 tokens 472 us, 128 x 128
-  // 526; 13 experts of 520 x 392 (78 tiles) 20.0, 128 x 128 12.5
+  // 526. Else 64 x 64, whose smaller tiles spread further (3 experts of 2048 x 256, 2667 rows each:
+  // 31.4 us, 128 x 128 45.4; 13 of 520 x 392, 256 rows 12.4 / 14.0), unless 128 x 128 makes enough
+  // tiles of many rows for its fewer reads to count (one of 1536 x 2048, 8192 rows 103 / 121).
   if (g.E * blocks(g.N, 256) * blocks(g.K, 256) >= 256) return launch_cfg<kDw, T, 2, 4, 4, 2, 32, 64, 4>(g, st);
-  return launch_cfg<kDw, T, 2, 2, 2, 2, 32, 64, 3>(g, st);
+  if (g.E * blocks(g.N, 128) * blocks(g.K, 128) >= 128 && g.P / g.E >= 1024)
+    return launch_cfg<kDw, T, 2, 2, 2, 2, 32, 64, 3>(g, st);
+  return launch_cfg<kDw, T, 2, 2, 1, 1, 32, 64, 4>(g, st);
 }
 
 hipError_t launch_grouped_dw(int type, const GroupedArgs& g, hipStream_t st) {

@@ -164,6 +164,7 @@ LOADS = {
     "256 x 256, one K-block": ([513, 1500], 1, 8200, 48),
     "gradients of few rows": ([1, 0, 3] * 80, 1, 264, 520),
     "gradients of many rows": ([1029, 2300, 31], 1, 520, 5640),
+    "weights, 128 x 128": ([1100, 3000, 0], 1, 776, 1032),
     "weights of many experts": ([1, 0, 70] * 90 + [2113], 1, 136, 72),
 }
 
